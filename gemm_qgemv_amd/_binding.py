@@ -21,13 +21,39 @@ QG_STATIC_SCRATCH_BYTES = 8 << 20
 QG_MAX_GEMV_BATCH = 16
 QG_MAX_ARGMAX_BATCH = 256
 QG_WS_CONTROL_BYTES = 8192
+QG_F32, QG_BF16 = 1, 2
+QG_MAX_PLAN_BATCH = 8192
+QG_MAX_TOP = 64
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqg.so")
 
 EXPORTS = ("qgemv", "qgemm", "qgemv_argmax", "qgemv_argmax_noalloc", "qembed",
-           "qg_workspace_bytes", "qg_status_str", "qg_abi_version")
+           "qg_workspace_bytes", "qg_status_str", "qg_abi_version",
+           "qkv_cache_bytes", "qkv_plan", "qkv_append", "qkv_read", "qkv_attn",
+           "qkv_attn_workspace_bytes", "qlogprobs", "qlogprobs_workspace_bytes")
 
 _lib = None
+
+
+class _KVCacheStruct(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class KVCache:
+    """The paged 4-bit key/value cache as the entry points take it
+    (qg_kv_cache): its device memory (a tensor, kept alive here, or an
+    address) and its geometry. `tensors.kv_cache` allocates one."""
+
+    def __init__(self, data, num_pages, page_size, kv_heads, head_dim):
+        self.data = data
+        self.num_pages, self.page_size = int(num_pages), int(page_size)
+        self.kv_heads, self.head_dim = int(kv_heads), int(head_dim)
+        self._struct = _KVCacheStruct(_ptr(data), self.num_pages, self.page_size, self.kv_heads, self.head_dim)
+        self._ref = ctypes.byref(self._struct)
+        need = lib().qkv_cache_bytes(self._ref)
+        if need and data is not None and not isinstance(data, int) and data.numel() * data.element_size() < need:
+            raise ValueError(f"the cache's memory has {data.numel() * data.element_size()} bytes, its geometry needs {need}")
 
 
 class QGError(RuntimeError):
@@ -56,8 +82,20 @@ def lib() -> ctypes.CDLL:
         L.qg_status_str.argtypes = [I32]
         L.qg_status_str.restype = ctypes.c_char_p
         L.qg_abi_version.argtypes = []
+        F = ctypes.c_float
+        L.qkv_cache_bytes.argtypes = [P]
+        L.qkv_plan.argtypes = [P, P, P, I32, I32, P, I64, P, I64, P, P, P, P, P, P, I64, P, P]
+        L.qkv_append.argtypes = [I32, P, I64, P, I64, P, I64, P, P]
+        L.qkv_read.argtypes = [I32, P, P, I64, P, I64, P, I64, P]
+        L.qkv_attn.argtypes = [I32, P, I64, P, P, I64, P, P, I32, I64, I64, I64, I32, F, I64, P, I64, P,
+                               P, SZ, P]
+        L.qkv_attn_workspace_bytes.argtypes = [P, I32, I64, I64, I64, I32]
+        L.qlogprobs.argtypes = [P, I64, I64, I64, P, I32, P, P, P, P, P, P, SZ, P]
+        L.qlogprobs_workspace_bytes.argtypes = [I64, I64, I32]
+        for f in (L.qkv_cache_bytes, L.qkv_attn_workspace_bytes, L.qlogprobs_workspace_bytes):
+            f.restype = SZ
         for f in (L.qgemv, L.qgemm, L.qgemv_argmax, L.qgemv_argmax_noalloc, L.qembed,
-                  L.qg_abi_version):
+                  L.qg_abi_version, L.qkv_plan, L.qkv_append, L.qkv_read, L.qkv_attn, L.qlogprobs):
             f.restype = I32
         _lib = L
     return _lib
@@ -119,6 +157,49 @@ def qgemv_argmax_noalloc(fmt, codes, scales, biases, x, logits, idx, M, K, batch
 def qembed(fmt, codes, scales, biases, ids, out, M, K, n, stream=None):
     _check(lib().qembed(fmt, _ptr(codes), _ptr(scales), _ptr(biases), _ptr(ids), _ptr(out),
                         M, K, n, _stream(stream)), "qembed")
+
+
+def qkv_cache_bytes(cache) -> int:
+    return int(lib().qkv_cache_bytes(cache._ref))
+
+
+def qkv_plan(len_old, keep, n_new, batch, page_size, block_table, table_stride, ring, ring_size, state_in,
+             state_out, kv_len, cu_q, slots, pos, total, denied, stream=None):
+    _check(lib().qkv_plan(_ptr(len_old), _ptr(keep), _ptr(n_new), batch, page_size, _ptr(block_table), table_stride,
+                          _ptr(ring), ring_size, _ptr(state_in), _ptr(state_out), _ptr(kv_len), _ptr(cu_q),
+                          _ptr(slots), _ptr(pos), total, _ptr(denied), _stream(stream)), "qkv_plan")
+
+
+def qkv_append(dtype, k, k_stride, v, v_stride, slots, n, cache, stream=None):
+    _check(lib().qkv_append(dtype, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(slots), n, cache._ref,
+                            _stream(stream)), "qkv_append")
+
+
+def qkv_read(dtype, cache, slots, n, k, k_stride, v, v_stride, stream=None):
+    _check(lib().qkv_read(dtype, cache._ref, _ptr(slots), n, _ptr(k), k_stride, _ptr(v), v_stride,
+                          _stream(stream)), "qkv_read")
+
+
+def qkv_attn(dtype, q, q_stride, cache, block_table, table_stride, cu_q, kv_len, batch, total_q, max_q, max_kv,
+             q_heads, scale, window, out, out_stride, lse=None, ws=None, ws_bytes=None, stream=None):
+    _check(lib().qkv_attn(dtype, _ptr(q), q_stride, cache._ref, _ptr(block_table), table_stride, _ptr(cu_q),
+                          _ptr(kv_len), batch, total_q, max_q, max_kv, q_heads, scale, window, _ptr(out),
+                          out_stride, _ptr(lse), _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream)), "qkv_attn")
+
+
+def qkv_attn_workspace_bytes(cache, batch, total_q, max_q, max_kv, q_heads) -> int:
+    return int(lib().qkv_attn_workspace_bytes(cache._ref, batch, total_q, max_q, max_kv, q_heads))
+
+
+def qlogprobs(logits, ld, rows, vocab, ids, top, logprob, entropy, rank, top_ids=None, top_logprobs=None,
+              ws=None, ws_bytes=None, stream=None):
+    _check(lib().qlogprobs(_ptr(logits), ld, rows, vocab, _ptr(ids), top, _ptr(logprob), _ptr(entropy), _ptr(rank),
+                           _ptr(top_ids), _ptr(top_logprobs), _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream)),
+           "qlogprobs")
+
+
+def qlogprobs_workspace_bytes(rows, vocab, top) -> int:
+    return int(lib().qlogprobs_workspace_bytes(rows, vocab, top))
 
 
 def qg_workspace_bytes(op, fmt, M, K, rows) -> int:

@@ -8,10 +8,14 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRC = os.path.join(HERE, "csrc", "qg.hip")
+# the low-bit products, and the serving-step operators
+SOURCES = [os.path.join(HERE, "csrc", "qg.hip"), os.path.join(HERE, "serve", "kv.hip"),
+           os.path.join(HERE, "serve", "attn.hip"), os.path.join(HERE, "serve", "logprobs.hip")]
 OUT = os.path.join(HERE, "libqg.so")
 PROBE_SRC = os.path.join(HERE, "csrc", "probe.hip")
 PROBE_OUT = os.path.join(HERE, "libqgprobe.so")
@@ -22,7 +26,6 @@ FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-Wall",
     # IEEE float32: no fast-math, fp32 denormals kept
     "-fno-fast-math",
@@ -34,14 +37,21 @@ FLAGS = [
 
 
 def build(out: str = OUT, extra: list[str] | None = None, verbose: bool = False) -> str:
-    """Build libqg.so and the measurement-only libqgprobe.so."""
-    _hipcc(PROBE_SRC, PROBE_OUT, extra, verbose)
-    return _hipcc(SRC, out, extra, verbose)
+    """Build libqg.so and the measurement-only libqgprobe.so. Sources are
+    compiled side by side."""
+    with tempfile.TemporaryDirectory() as tmp:
+        objects = [os.path.join(tmp, f"{i}.o") for i in range(len(SOURCES))]
+        jobs = [(["-c", src], obj) for src, obj in zip(SOURCES, objects)]
+        jobs.append((["-shared", PROBE_SRC], PROBE_OUT))
+        with ThreadPoolExecutor(max_workers=len(jobs)) as pool:
+            for done in [pool.submit(_hipcc, what, to, extra, verbose) for what, to in jobs]:
+                done.result()
+        return _hipcc(["-shared", *objects], out, extra, verbose)
 
 
-def _hipcc(src: str, out: str, extra: list[str] | None, verbose: bool) -> str:
+def _hipcc(what: list[str], out: str, extra: list[str] | None, verbose: bool) -> str:
     tmp = out + ".tmp"
-    cmd = [HIPCC, *FLAGS, *(extra or []), src, "-o", tmp]
+    cmd = [HIPCC, *FLAGS, *(extra or []), *what, "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)

@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "../../include/qg.h"
+#include "host_args.hpp"
 #include "embed.hpp"
 #include "gemm.hpp"
 #include "gemv.hpp"
@@ -37,9 +38,6 @@ constexpr int64_t kLdsBudget = 96 * 1024;
 // workgroup per compute unit and keeps the whole activation operand there.
 constexpr int64_t kLdsMax = 160 * 1024;
 constexpr int64_t kLdsStaticReserve = 1024;   // static LDS of a kernel (keys, flags)
-// Compute units of the MI355X (one small-batch matrix-core workgroup each).
-constexpr int64_t kComputeUnits = 256;
-constexpr int64_t kAlign = 16;
 constexpr int kThreads = 256;
 
 bool known_format(int fmt)
@@ -71,12 +69,6 @@ int64_t bias_bytes(int fmt, int64_t M, int64_t K)
     return fmt == QG_U4_G64 ? 2 * M * (K / 64) : 0;
 }
 
-bool aligned(const void *p, int64_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
-size_t align256(size_t n) { return (n + 255) / 256 * 256; }
-
 // ---------------------------------------------------------------------------
 // argument checks (host only, before anything is enqueued)
 // ---------------------------------------------------------------------------
@@ -92,38 +84,6 @@ int check_weights(int fmt, const void *codes, const void *scales, const void *bi
         (biases && !aligned(biases, kAlign)))
         return QG_ERR_ALIGN;
     return QG_OK;
-}
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void *p, int64_t bytes)
-{
-    uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return Range{a, a + static_cast<uintptr_t>(bytes)};
-}
-
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
-
-// Every written range must be disjoint from every input range and from
-// every other written range (an exact alias such as y == x is an overlap
-// like any other).
-int check_alias(const Range *inputs, int n_inputs, const Range *written, int n_written)
-{
-    for (int i = 0; i < n_written; ++i)
-        for (int j = 0; j < n_inputs; ++j)
-            if (overlap(written[i], inputs[j])) return QG_ERR_ALIAS;
-    for (int i = 0; i < n_written; ++i)
-        for (int j = i + 1; j < n_written; ++j)
-            if (overlap(written[i], written[j])) return QG_ERR_ALIAS;
-    return QG_OK;
-}
-
-int launch_status()
-{
-    hipError_t e = hipGetLastError();
-    return e == hipSuccess ? QG_OK : QG_ERR_LAUNCH;
 }
 
 // ---------------------------------------------------------------------------
@@ -1438,10 +1398,10 @@ const char *qg_status_str(int status)
     switch (status) {
     case QG_OK: return "ok";
     case QG_ERR_NULL: return "a required pointer is NULL (or biases given for a format without them)";
-    case QG_ERR_FORMAT: return "unknown weight format";
-    case QG_ERR_SHAPE: return "M, K or rows out of range, or K not a multiple of the format's unit";
+    case QG_ERR_FORMAT: return "unknown weight format or element type";
+    case QG_ERR_SHAPE: return "a size, stride or count out of range or not a multiple of its unit";
     case QG_ERR_ALIGN: return "a pointer is not aligned as required";
-    case QG_ERR_WORKSPACE: return "workspace missing or smaller than qg_workspace_bytes()";
+    case QG_ERR_WORKSPACE: return "workspace missing or smaller than the workspace query says";
     case QG_ERR_ALIAS: return "a written buffer overlaps another buffer";
     case QG_ERR_LAUNCH: return "kernel launch failed";
     case QG_ERR_UNSUPPORTED: return "format not implemented by this entry point";

@@ -1,0 +1,189 @@
+// attn.hip -- entry point of attention over the paged 4-bit cache: checks,
+// the choice of kernel and of the split of the tokens, launches.
+#include "kv_host.hpp"
+
+#include <cmath>
+
+#include <algorithm>
+
+#include "attn.hpp"
+
+namespace {
+
+// A call's launch geometry: a pure function of sizes known on the host.
+struct AttnPlan {
+    int rows;              // query rows of a workgroup
+    int rw, qt;            // row groups of waves, 16-row tiles a wave
+    int64_t slots;         // tile slots
+    int nsplit;
+    int32_t chunk;
+};
+
+// Row groups: decode steps (up to 16 rows a request and key/value head) give
+// all four waves to the tokens; the more rows, the more waves take rows, so
+// that a fetched tile serves all of them.
+AttnPlan plan_attn(const qg_kv_cache &c, int batch, int64_t total_q, int64_t max_q, int64_t max_kv, int q_heads)
+{
+    const int group = q_heads / c.kv_heads;
+    const int64_t most = std::min(max_q, total_q) * group;
+    AttnPlan a;
+    a.rw = most <= 16 ? 1 : most <= 32 ? 2 : 4;
+    a.qt = most > 64 && c.head_dim <= 128 ? 2 : 1;
+    a.rows = 16 * a.rw * a.qt;
+    a.slots = total_q * group / a.rows + batch;
+    const int step = qg::attn_tile_tokens(c.head_dim, a.qt) * (4 / a.rw);     // tokens of a workgroup's round of tiles
+    // enough workgroups for two on every compute unit, twice over
+    const int64_t tiles = std::max<int64_t>(1, total_q * group / a.rows);
+    const int64_t have = std::max(tiles, std::min<int64_t>(batch, total_q)) * c.kv_heads;
+    const int64_t want = ceil_div(4 * kComputeUnits, have);
+    const int64_t most_splits = ceil_div(max_kv, step);
+    a.nsplit = static_cast<int>(std::clamp<int64_t>(want, 1, std::min<int64_t>(most_splits, 256)));
+    // a window's or a tile's first token is rounded down to a tile: one more
+    a.chunk = static_cast<int32_t>(round_up(ceil_div(max_kv + qg::attn_tile_tokens(c.head_dim, a.qt), a.nsplit), step));
+    a.nsplit = static_cast<int>(ceil_div(max_kv + qg::attn_tile_tokens(c.head_dim, a.qt), a.chunk));
+    return a;
+}
+
+// With a window a tile of rows sees at most window + rows tokens: as many
+// splits, of fewer tokens.
+void narrow_plan(AttnPlan &a, const qg_kv_cache &c, int64_t max_kv, int64_t window)
+{
+    if (window >= max_kv) return;
+    const int tile = qg::attn_tile_tokens(c.head_dim, a.qt), step = tile * (4 / a.rw);
+    const int64_t range = std::min<int64_t>(max_kv, window + a.rows) + tile;
+    a.chunk = static_cast<int32_t>(round_up(ceil_div(range, a.nsplit), step));
+    a.nsplit = static_cast<int>(ceil_div(range, a.chunk));
+}
+
+size_t attn_workspace(const AttnPlan &a, const qg_kv_cache &c, int64_t total_q, int q_heads)
+{
+    if (a.nsplit == 1) return 0;
+    return align256(static_cast<size_t>(total_q) * q_heads * a.nsplit * (c.head_dim + 2) * 4);
+}
+
+int check_attn_sizes(const qg_kv_cache &c, int batch, int64_t total_q, int64_t max_q, int64_t max_kv, int q_heads)
+{
+    if (batch < 1 || batch > 65535 || total_q < 1 || total_q > 0x7fffffffLL || max_q < 1 || max_kv < 1 ||
+        max_kv > (int64_t(1) << 30) || q_heads < 1 || q_heads > 1024 || q_heads % c.kv_heads != 0)
+        return QG_ERR_SHAPE;
+    const AttnPlan a = plan_attn(c, batch, total_q, max_q, max_kv, q_heads);
+    const int64_t rows = total_q * q_heads;
+    return a.slots * c.kv_heads > 0x7fffffffLL || ceil_div(rows, 4) > 0x7fffffffLL ? QG_ERR_SHAPE : QG_OK;
+}
+
+template <typename T, int D, int RW, int QT>
+void launch_attn(const AttnPlan &a, const qg::AttnParams &p, hipStream_t s)
+{
+    constexpr int KW = 4 / RW;
+    constexpr int lds = qg::attn_lds_bytes<D, RW, KW, QT>();
+    auto kernel = qg::attn_kernel<T, D, RW, KW, QT>;
+    static const bool allowed = [&] {
+        return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds) ==
+               hipSuccess;
+    }();
+    (void)allowed;
+    const dim3 grid(static_cast<unsigned>(a.slots * p.kv.heads), static_cast<unsigned>(a.nsplit));
+    hipLaunchKernelGGL(kernel, grid, dim3(qg::kAttnThreads), lds, s, p);
+    if (a.nsplit > 1)
+        hipLaunchKernelGGL((qg::attn_join_kernel<T, D, 16 * RW * QT, qg::attn_tile_tokens(D, QT)>), dim3(static_cast<unsigned>(ceil_div(p.total_q * p.q_heads, 4))),
+                           dim3(256), 0, s, p);
+}
+
+template <typename T, int D>
+void launch_attn_dim(const AttnPlan &a, const qg::AttnParams &p, hipStream_t s)
+{
+    if (a.rw == 1) launch_attn<T, D, 1, 1>(a, p, s);
+    else if (a.rw == 2) launch_attn<T, D, 2, 1>(a, p, s);
+    else if (a.qt == 1) launch_attn<T, D, 4, 1>(a, p, s);
+    else if constexpr (D <= 128) launch_attn<T, D, 4, 2>(a, p, s);
+}
+
+template <typename T>
+void launch_attn_type(const AttnPlan &a, const qg::AttnParams &p, hipStream_t s)
+{
+    if (p.kv.dim == 64) launch_attn_dim<T, 64>(a, p, s);
+    else if (p.kv.dim == 128) launch_attn_dim<T, 128>(a, p, s);
+    else launch_attn_dim<T, 256>(a, p, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qkv_attn_workspace_bytes(const qg_kv_cache *cache, int batch, int64_t total_q, int64_t max_q,
+                                int64_t max_kv, int q_heads)
+{
+    if (!cache || check_geometry(*cache) != QG_OK) return 0;
+    if (check_attn_sizes(*cache, batch, total_q, max_q, max_kv, q_heads) != QG_OK) return 0;
+    return attn_workspace(plan_attn(*cache, batch, total_q, max_q, max_kv, q_heads), *cache, total_q, q_heads);
+}
+
+int qkv_attn(int dtype, const void *q, int64_t q_stride, const qg_kv_cache *cache,
+             const int32_t *block_table, int64_t table_stride, const int32_t *cu_q,
+             const int32_t *kv_len, int batch, int64_t total_q, int64_t max_q, int64_t max_kv,
+             int q_heads, float scale, int64_t window, void *out, int64_t out_stride, float *lse,
+             void *ws, size_t ws_bytes, hipStream_t stream)
+{
+    if (!known_dtype(dtype)) return QG_ERR_FORMAT;
+    if (!q || !cache || !cache->data || !block_table || !cu_q || !kv_len || !out) return QG_ERR_NULL;
+    int st = check_cache(*cache);
+    if (st != QG_OK) return st;
+    if ((st = check_attn_sizes(*cache, batch, total_q, max_q, max_kv, q_heads)) != QG_OK) return st;
+    if (table_stride < 1 || table_stride > 0x7fffffffLL || max_kv > table_stride * cache->page_size || window < 0 ||
+        !(scale > 0.0f) || !std::isfinite(scale * 1.5f))
+        return QG_ERR_SHAPE;
+    const int size = dtype == QG_F32 ? 4 : 2;
+    const int64_t width = int64_t(q_heads) * cache->head_dim;
+    for (const int64_t stride : {q_stride, out_stride})
+        if (stride < width || stride > (int64_t(1) << 40) || stride * size % kAlign != 0) return QG_ERR_SHAPE;
+    if (!aligned(q, kAlign) || !aligned(out, kAlign) || !aligned(block_table, 4) || !aligned(cu_q, 4) ||
+        !aligned(kv_len, 4) || (lse && !aligned(lse, 4)))
+        return QG_ERR_ALIGN;
+    AttnPlan a = plan_attn(*cache, batch, total_q, max_q, max_kv, q_heads);
+    if (window > 0) narrow_plan(a, *cache, max_kv, window);
+    const size_t need = attn_workspace(a, *cache, total_q, q_heads);
+    if (need > 0) {
+        if (!ws || ws_bytes < need) return QG_ERR_WORKSPACE;
+        if (!aligned(ws, kAlign)) return QG_ERR_ALIGN;
+    }
+    const Range inputs[5] = {range_of(q, ((total_q - 1) * q_stride + width) * size),
+                             range_of(cache->data, cache_bytes(*cache)), range_of(block_table, batch * table_stride * 4),
+                             range_of(cu_q, (int64_t(batch) + 1) * 4), range_of(kv_len, int64_t(batch) * 4)};
+    Range written[3];
+    int nw = 0;
+    written[nw++] = range_of(out, ((total_q - 1) * out_stride + width) * size);
+    if (lse) written[nw++] = range_of(lse, total_q * q_heads * 4);
+    if (need > 0) written[nw++] = range_of(ws, static_cast<int64_t>(need));
+    if ((st = check_alias(inputs, 5, written, nw)) != QG_OK) return st;
+
+    (void)hipGetLastError();
+    qg::AttnParams p{};
+    p.q = q;
+    p.q_stride = q_stride;
+    p.kv = kv_view(*cache);
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.cu_q = cu_q;
+    p.kv_len = kv_len;
+    p.batch = batch;
+    p.total_q = total_q;
+    p.max_kv = static_cast<int32_t>(max_kv);
+    p.group = q_heads / cache->kv_heads;
+    p.q_heads = q_heads;
+    p.scale_log2e = scale * 1.44269504088896340736f;
+    p.window = window > max_kv ? 0 : window;
+    p.out = out;
+    p.out_stride = out_stride;
+    p.lse = lse;
+    p.nsplit = a.nsplit;
+    p.chunk = a.chunk;
+    if (a.nsplit > 1) {
+        p.part_out = static_cast<float *>(ws);
+        p.part_stat = p.part_out + total_q * q_heads * a.nsplit * cache->head_dim;
+    }
+    if (dtype == QG_F32) launch_attn_type<float>(a, p, stream);
+    else launch_attn_type<uint16_t>(a, p, stream);
+    return launch_status();
+}
+
+}  // extern "C"

@@ -1,0 +1,153 @@
+// kv.hip -- entry points of the paged 4-bit key/value cache: its size, the
+// page plan of a step, append and read-back. Host-side checks and launches;
+// the arithmetic is in plan.hpp and append.hpp.
+#include "kv_host.hpp"
+
+#include <algorithm>
+
+#include "append.hpp"
+#include "plan.hpp"
+
+namespace {
+
+// Rows of activations: `n` rows `stride` elements apart, `width` used.
+int check_rows(int dtype, const void *p, int64_t stride, int64_t width)
+{
+    const int size = dtype == QG_F32 ? 4 : 2;
+    if (stride < width || stride > (int64_t(1) << 40) || stride * size % kAlign != 0) return QG_ERR_SHAPE;
+    return aligned(p, kAlign) ? QG_OK : QG_ERR_ALIGN;
+}
+
+Range rows_range(int dtype, const void *p, int64_t stride, int64_t width, int64_t n)
+{
+    return range_of(p, ((n - 1) * stride + width) * (dtype == QG_F32 ? 4 : 2));
+}
+
+qg::AppendMap append_map(const qg_kv_cache &c, int64_t n, dim3 &grid)
+{
+    qg::AppendMap m;
+    m.per_row = c.kv_heads * c.head_dim / 8;
+    m.rows = std::max(1, qg::kAppendThreads / m.per_row);
+    m.inv = 1.0f / static_cast<float>(m.per_row);
+    grid = dim3(static_cast<unsigned>(ceil_div(n, m.rows)), 2,
+                static_cast<unsigned>(ceil_div(m.per_row, qg::kAppendThreads)));
+    return m;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qkv_cache_bytes(const qg_kv_cache *cache)
+{
+    if (!cache || check_geometry(*cache) != QG_OK) return 0;
+    return static_cast<size_t>(cache_bytes(*cache));
+}
+
+int qkv_plan(const int32_t *len_old, const int32_t *keep, const int32_t *n_new, int batch,
+             int page_size, int32_t *block_table, int64_t table_stride, int32_t *ring,
+             int64_t ring_size, const int64_t *state_in, int64_t *state_out, int32_t *kv_len,
+             int32_t *cu_q, int32_t *slots, int32_t *pos, int64_t total, int32_t *denied,
+             hipStream_t stream)
+{
+    if (!len_old || !keep || !n_new || !block_table || !ring || !state_in || !state_out || !kv_len ||
+        !cu_q || !denied || (total > 0 && (!slots || !pos)))
+        return QG_ERR_NULL;
+    if (batch < 1 || batch > QG_MAX_PLAN_BATCH || page_size < 1 || page_size > (1 << 20) ||
+        (page_size & (page_size - 1)) != 0 || table_stride < 1 || table_stride > 0x7fffffffLL ||
+        ring_size < 1 || ring_size > 0x7fffffffLL || total < 0 || total > 0x7fffffffLL)
+        return QG_ERR_SHAPE;
+    for (const void *p : {static_cast<const void *>(len_old), static_cast<const void *>(keep),
+                          static_cast<const void *>(n_new), static_cast<const void *>(block_table),
+                          static_cast<const void *>(ring), static_cast<const void *>(kv_len),
+                          static_cast<const void *>(cu_q), static_cast<const void *>(slots),
+                          static_cast<const void *>(pos), static_cast<const void *>(denied)})
+        if (!aligned(p, 4)) return QG_ERR_ALIGN;
+    if (!aligned(state_in, 8) || !aligned(state_out, 8)) return QG_ERR_ALIGN;
+    const Range inputs[4] = {range_of(len_old, int64_t(batch) * 4), range_of(keep, int64_t(batch) * 4),
+                             range_of(n_new, int64_t(batch) * 4), range_of(state_in, 16)};
+    const Range written[8] = {range_of(block_table, batch * table_stride * 4), range_of(ring, ring_size * 4),
+                              range_of(state_out, 16), range_of(kv_len, int64_t(batch) * 4),
+                              range_of(cu_q, (int64_t(batch) + 1) * 4), range_of(denied, 4),
+                              range_of(slots, total * 4), range_of(pos, total * 4)};
+    const int st = check_alias(inputs, 4, written, 8);
+    if (st != QG_OK) return st;
+
+    (void)hipGetLastError();
+    qg::PlanParams p{len_old, keep, n_new, batch, __builtin_ctz(static_cast<unsigned>(page_size)), block_table,
+                     table_stride, ring, ring_size, state_in, state_out, kv_len, cu_q, slots, pos, total, denied};
+    // eight tokens a thread: every workgroup repeats the running sums
+    const auto grid = static_cast<unsigned>(std::clamp<int64_t>(ceil_div(total, qg::kPlanThreads * 8), 1, 256));
+    const size_t lds = (3 * static_cast<size_t>(batch) + 1) * 4;
+    static const bool allowed = [] {
+        return hipFuncSetAttribute(reinterpret_cast<const void *>(qg::kv_plan_kernel),
+                                   hipFuncAttributeMaxDynamicSharedMemorySize, (3 * QG_MAX_PLAN_BATCH + 1) * 4) == hipSuccess;
+    }();
+    (void)allowed;
+    hipLaunchKernelGGL(qg::kv_plan_kernel, dim3(grid), dim3(qg::kPlanThreads), lds, stream, p);
+    return launch_status();
+}
+
+int qkv_append(int dtype, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+               const int32_t *slots, int64_t n, const qg_kv_cache *cache, hipStream_t stream)
+{
+    if (!known_dtype(dtype)) return QG_ERR_FORMAT;
+    if (!cache || !cache->data) return QG_ERR_NULL;
+    if (n > 0 && (!k || !v || !slots)) return QG_ERR_NULL;
+    int st = check_cache(*cache);
+    if (st != QG_OK) return st;
+    if (n < 0 || n > 0x7fffffffLL) return QG_ERR_SHAPE;
+    if (n == 0) return QG_OK;
+    const int64_t width = int64_t(cache->kv_heads) * cache->head_dim;
+    if ((st = check_rows(dtype, k, k_stride, width)) != QG_OK) return st;
+    if ((st = check_rows(dtype, v, v_stride, width)) != QG_OK) return st;
+    if (!aligned(slots, 4)) return QG_ERR_ALIGN;
+    const Range inputs[3] = {rows_range(dtype, k, k_stride, width, n), rows_range(dtype, v, v_stride, width, n),
+                             range_of(slots, n * 4)};
+    const Range written[1] = {range_of(cache->data, cache_bytes(*cache))};
+    if ((st = check_alias(inputs, 3, written, 1)) != QG_OK) return st;
+
+    (void)hipGetLastError();
+    dim3 grid;
+    const qg::AppendMap map = append_map(*cache, n, grid);
+    qg::AppendParams p{{k, v}, {k_stride, v_stride}, slots, n, map, kv_view(*cache)};
+    if (dtype == QG_F32)
+        hipLaunchKernelGGL(qg::kv_append_kernel<float>, grid, dim3(qg::kAppendThreads), 0, stream, p);
+    else
+        hipLaunchKernelGGL(qg::kv_append_kernel<uint16_t>, grid, dim3(qg::kAppendThreads), 0, stream, p);
+    return launch_status();
+}
+
+int qkv_read(int dtype, const qg_kv_cache *cache, const int32_t *slots, int64_t n, void *k,
+             int64_t k_stride, void *v, int64_t v_stride, hipStream_t stream)
+{
+    if (!known_dtype(dtype)) return QG_ERR_FORMAT;
+    if (!cache || !cache->data) return QG_ERR_NULL;
+    if (n > 0 && (!slots || (!k && !v))) return QG_ERR_NULL;
+    int st = check_cache(*cache);
+    if (st != QG_OK) return st;
+    if (n < 0 || n > 0x7fffffffLL) return QG_ERR_SHAPE;
+    if (n == 0) return QG_OK;
+    const int64_t width = int64_t(cache->kv_heads) * cache->head_dim;
+    if (k && (st = check_rows(dtype, k, k_stride, width)) != QG_OK) return st;
+    if (v && (st = check_rows(dtype, v, v_stride, width)) != QG_OK) return st;
+    if (!aligned(slots, 4)) return QG_ERR_ALIGN;
+    const Range inputs[2] = {range_of(cache->data, cache_bytes(*cache)), range_of(slots, n * 4)};
+    Range written[2];
+    int nw = 0;
+    if (k) written[nw++] = rows_range(dtype, k, k_stride, width, n);
+    if (v) written[nw++] = rows_range(dtype, v, v_stride, width, n);
+    if ((st = check_alias(inputs, 2, written, nw)) != QG_OK) return st;
+
+    (void)hipGetLastError();
+    dim3 grid;
+    const qg::AppendMap map = append_map(*cache, n, grid);
+    qg::ReadParams p{{k, v}, {k_stride, v_stride}, slots, n, map, kv_view(*cache)};
+    if (dtype == QG_F32)
+        hipLaunchKernelGGL(qg::kv_read_kernel<float>, grid, dim3(qg::kAppendThreads), 0, stream, p);
+    else
+        hipLaunchKernelGGL(qg::kv_read_kernel<uint16_t>, grid, dim3(qg::kAppendThreads), 0, stream, p);
+    return launch_status();
+}
+
+}  // extern "C"

@@ -1,0 +1,320 @@
+// logprobs.hpp -- log probabilities of given tokens, entropy, rank and the
+// best alternatives of rows of logits, in one pass over them.
+//
+// With a running maximum m a lane keeps z = sum e^(x - m) and
+// t = sum e^(x - m) (x - m); a new maximum m' scales them by a = e^(m - m'):
+// z' = a z, t' = a (t + z (m - m')). Then with z, t, m of the whole row
+//   log p[i] = (x[i] - m) - log z,    entropy = log z - t / z.
+// m starts at the lowest finite value, so rows and parts of rows of
+// -infinity need no test: their terms are 0.
+//
+// The order of the alternatives (larger logit first, ties by lower index) is
+// that of the 64-bit keys argmax_key(x, index). A wave keeps its best 64 keys
+// sorted over its lanes; a block of 1024 logits is looked at for them only if
+// its maximum passes the last one wanted, which gets rare soon (a block is
+// one of n equal blocks so far: about top / n). The block's candidates, one a
+// lane, are sorted and merged into the list by bitonic networks over lanes.
+//
+// A row is cut into slices over workgroups, each slice into runs of blocks
+// over 4 waves; the parts are joined over LDS and, with more than one slice,
+// by a second launch, in a fixed order.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../csrc/qg_device.hpp"
+#include "kv_cache.hpp"
+
+namespace qg {
+
+struct LogprobParams {
+    const float *x;
+    int64_t ld, rows;
+    int32_t vocab;
+    const int32_t *ids;
+    int top;
+    float *logprob, *entropy;
+    int32_t *rank, *top_ids;
+    float *top_logprobs;
+    f32x4 *part;                 // [rows][nslice]: m, z, t, count (as bits)
+    uint64_t *part_keys;         // [rows][nslice][top]
+    int nslice;
+    int32_t slice;               // logits of a slice (a multiple of kLpBlock * kLpWaves)
+};
+
+constexpr int kLpThreads = 256;
+constexpr int kLpWaves = kLpThreads / 64;
+constexpr int kLpQuads = 4;                          // 16-byte loads a lane has in flight
+constexpr int kLpBlock = 64 * 4 * kLpQuads;          // logits a wave takes at a time
+constexpr float kLowest = -3.402823466e38f;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct Moments {
+    float m, z, t;
+};
+
+__device__ __forceinline__ Moments lp_join(Moments a, Moments b)
+{
+    const float m = fmaxf(a.m, b.m);
+    const float fa = __builtin_amdgcn_exp2f((a.m - m) * kLog2e), fb = __builtin_amdgcn_exp2f((b.m - m) * kLog2e);
+    // an infinite difference of maxima belongs to a side that scales to 0
+    const float da = fmaxf(a.m - m, -1000.0f), db = fmaxf(b.m - m, -1000.0f);
+    return {m, fmaf(fa, a.z, fb * b.z), fmaf(fa, fmaf(a.z, da, a.t), fb * fmaf(b.z, db, b.t))};
+}
+
+__device__ __forceinline__ uint64_t key_max(uint64_t a, uint64_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint64_t key_min(uint64_t a, uint64_t b) { return a < b ? a : b; }
+
+// Keys of a bitonic sequence over the 64 lanes into descending order.
+__device__ __forceinline__ uint64_t bitonic_merge(uint64_t k, int lane)
+{
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+        const uint64_t o = shfl_xor_u64(k, d);
+        k = lane & d ? key_min(k, o) : key_max(k, o);
+    }
+    return k;
+}
+
+// Any 64 keys into descending order over the lanes.
+__device__ __forceinline__ uint64_t bitonic_sort(uint64_t k, int lane)
+{
+#pragma unroll
+    for (int w = 2; w <= 64; w <<= 1)
+#pragma unroll
+        for (int d = w >> 1; d >= 1; d >>= 1) {
+            const uint64_t o = shfl_xor_u64(k, d);
+            const bool keep_max = ((lane & d) == 0) == ((lane & w) == 0);
+            k = keep_max ? key_max(k, o) : key_min(k, o);
+        }
+    return k;
+}
+
+// The 64 largest of two descending lists, descending.
+__device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b, int lane)
+{
+    const uint64_t r = shfl_xor_u64(b, 63);          // reversed
+    return bitonic_merge(key_max(a, r), lane);
+}
+
+__device__ __forceinline__ uint64_t lane_u64(uint64_t v, int src)
+{
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(v), src);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(v >> 32), src);
+    return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+
+__device__ __forceinline__ float key_value(uint64_t key)
+{
+    const uint32_t u = static_cast<uint32_t>(key >> 32);
+    return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
+
+struct RowResult {
+    Moments mo;
+    int32_t before;              // tokens before the given one
+    uint64_t list;               // lane i: the i-th best key
+};
+
+// The results of the workgroup's waves joined, in every wave.
+__device__ __forceinline__ RowResult lp_join_waves(RowResult r, bool want_top)
+{
+    __shared__ f32x4 stat[kLpWaves];
+    __shared__ uint64_t lists[kLpWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __syncthreads();
+    if (lane == 0) stat[wave] = f32x4{r.mo.m, r.mo.z, r.mo.t, __int_as_float(r.before)};
+    if (want_top) lists[wave][lane] = r.list;
+    __syncthreads();
+    RowResult o;
+    o.mo = {kLowest, 0.0f, 0.0f};
+    o.before = 0;
+    o.list = 0;
+#pragma unroll
+    for (int w = 0; w < kLpWaves; ++w) {
+        const f32x4 s = stat[w];
+        o.mo = lp_join(o.mo, {s[0], s[1], s[2]});
+        o.before += __float_as_int(s[3]);
+    }
+    if (want_top && wave == 0) {
+        o.list = lists[0][lane];
+#pragma unroll
+        for (int w = 1; w < kLpWaves; ++w) o.list = merge_lists(o.list, lists[w][lane], lane);
+    }
+    return o;
+}
+
+// Results of a whole row written (by wave 0).
+__device__ __forceinline__ void lp_finish(const LogprobParams &p, int64_t row, const RowResult &r)
+{
+    const int lane = threadIdx.x & 63;
+    if (threadIdx.x >= 64) return;
+    const float nan = __builtin_nanf("");
+    const float log_z = r.mo.z > 0.0f ? logf(r.mo.z) : nan;      // NaN too where z is NaN
+    if (lane == 0) {
+        if (p.entropy) p.entropy[row] = log_z - r.mo.t / r.mo.z;
+        if (p.ids) {
+            const int32_t id = p.ids[row];
+            const bool in = id >= 0 && id < p.vocab;
+            if (p.logprob) p.logprob[row] = in ? (p.x[row * p.ld + id] - r.mo.m) - log_z : nan;
+            if (p.rank) p.rank[row] = in ? r.before + 1 : 0;
+        }
+    }
+    if (lane < p.top) {
+        // fewer keys than `top` only where the row holds NaNs
+        const uint32_t id = argmax_key_index(r.list);
+        p.top_ids[row * p.top + lane] = static_cast<int32_t>(id < static_cast<uint32_t>(p.vocab) ? id : 0);
+        p.top_logprobs[row * p.top + lane] = (key_value(r.list) - r.mo.m) - log_z;
+    }
+}
+
+__global__ __launch_bounds__(kLpThreads) void logprob_kernel(LogprobParams p)
+{
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t row = blockIdx.x / static_cast<unsigned>(p.nslice);
+    const int slice = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.nslice));
+    const float *x = p.x + row * p.ld;
+    // positions count from the 16-byte boundary at or before the row's start
+    const int32_t skew = static_cast<int32_t>((reinterpret_cast<uintptr_t>(x) >> 2) & 3);
+    const int64_t span = int64_t(p.vocab) + skew;
+    const int64_t begin = int64_t(slice) * p.slice + int64_t(wave) * (p.slice / kLpWaves);
+    int64_t end = begin + p.slice / kLpWaves;
+    end = end < span ? end : span;
+
+    int32_t id = -1;
+    float given = 0.0f;
+    if (p.ids) {
+        id = p.ids[row];
+        if (id < 0 || id >= p.vocab) id = -1;
+        else given = x[id];
+    }
+    const int top = p.top;
+    RowResult r;
+    r.mo = {kLowest, 0.0f, 0.0f};
+    r.before = 0;
+    r.list = 0;
+    uint64_t last_key = 0;                 // the worst key wanted so far (0: the list is not full)
+    float last = 0.0f;
+
+    for (int64_t base = begin; base < end; base += kLpBlock) {
+        // the index of element e of quad j: at(j) + e
+        auto at = [&](int j) { return static_cast<int32_t>(base + j * 256 - skew) + lane * 4; };
+        const bool inner = base >= skew && base + kLpBlock <= span;
+        f32x4 v[kLpQuads];
+        if (inner) {
+#pragma unroll
+            for (int j = 0; j < kLpQuads; ++j) v[j] = *reinterpret_cast<const f32x4 *>(x + at(j));
+        } else {
+#pragma unroll
+            for (int j = 0; j < kLpQuads; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int32_t i = at(j) + e;
+                    v[j][e] = i >= 0 && i < p.vocab ? x[i] : -__builtin_inff();
+                }
+        }
+        float bm = v[0][0];
+#pragma unroll
+        for (int j = 0; j < kLpQuads; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bm = fmaxf(bm, v[j][e]);
+
+        const float m = fmaxf(r.mo.m, bm);
+        const float a = __builtin_amdgcn_exp2f((r.mo.m - m) * kLog2e), da = fmaxf(r.mo.m - m, -1000.0f);
+        r.mo.t = a * fmaf(r.mo.z, da, r.mo.t);
+        r.mo.z *= a;
+        r.mo.m = m;
+#pragma unroll
+        for (int j = 0; j < kLpQuads; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float d = v[j][e] - m;
+                const float w = __builtin_amdgcn_exp2f(d * kLog2e);
+                r.mo.z += w;
+                r.mo.t = fmaf(w, fmaxf(d, -1000.0f), r.mo.t);     // -infinity: 0 * -1000
+            }
+
+        if (id >= 0) {
+            const int32_t lo = static_cast<int32_t>(base - skew);
+            if (inner && lo + kLpBlock <= id) {
+#pragma unroll
+                for (int j = 0; j < kLpQuads; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) r.before += __popcll(__ballot(v[j][e] >= given));
+            } else if (inner && lo > id) {
+#pragma unroll
+                for (int j = 0; j < kLpQuads; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) r.before += __popcll(__ballot(v[j][e] > given));
+            } else {
+#pragma unroll
+                for (int j = 0; j < kLpQuads; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int32_t i = at(j) + e;
+                        const bool in = i >= 0 && i < p.vocab;
+                        r.before += __popcll(__ballot(in && (v[j][e] > given || (v[j][e] == given && i < id))));
+                    }
+            }
+        }
+
+        if (top > 0 && (last_key == 0 || __any(bm > last))) {
+            uint64_t used = ~0ull;                   // this lane's keys from here on are below
+            for (;;) {
+                uint64_t best = 0;
+#pragma unroll
+                for (int j = 0; j < kLpQuads; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int32_t i = at(j) + e;
+                        const bool in = inner || (i >= 0 && i < p.vocab);
+                        const uint64_t k = in ? argmax_key(v[j][e], static_cast<uint32_t>(i)) : 0;
+                        best = k < used && k > last_key ? key_max(best, k) : best;
+                    }
+                if (!__any(best != 0)) break;
+                used = best;
+                r.list = merge_lists(r.list, bitonic_sort(best, lane), lane);
+                last_key = lane_u64(r.list, top - 1);
+                last = key_value(last_key);
+            }
+        }
+    }
+
+    // lanes joined
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+        const Moments o = {lane_xor_f32(r.mo.m, d), lane_xor_f32(r.mo.z, d), lane_xor_f32(r.mo.t, d)};
+        // both partners add in the same order
+        r.mo = lane & d ? lp_join(o, r.mo) : lp_join(r.mo, o);
+    }
+    r = lp_join_waves(r, top > 0);
+    if (p.nslice == 1) {
+        lp_finish(p, row, r);
+    } else if (wave == 0) {
+        if (lane == 0) p.part[blockIdx.x] = f32x4{r.mo.m, r.mo.z, r.mo.t, __int_as_float(r.before)};
+        if (lane < top) p.part_keys[int64_t(blockIdx.x) * top + lane] = r.list;
+    }
+}
+
+// Joins the slices of a row.
+__global__ __launch_bounds__(kLpThreads) void logprob_join_kernel(LogprobParams p)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t row = blockIdx.x;
+    RowResult r;
+    r.mo = {kLowest, 0.0f, 0.0f};
+    r.before = 0;
+    r.list = 0;
+    for (int s = wave; s < p.nslice; s += kLpWaves) {
+        const int64_t at = row * p.nslice + s;
+        const f32x4 v = p.part[at];
+        r.mo = lp_join(r.mo, {v[0], v[1], v[2]});
+        r.before += __float_as_int(v[3]);
+        if (p.top > 0) r.list = merge_lists(r.list, lane < p.top ? p.part_keys[at * p.top + lane] : 0, lane);
+    }
+    r = lp_join_waves(r, p.top > 0);
+    lp_finish(p, row, r);
+}
+
+}  // namespace qg

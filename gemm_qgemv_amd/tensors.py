@@ -50,3 +50,27 @@ def workspace(op: int, fmt: int, M: int, K: int, rows: int, device="cuda"):
     if n == 0:
         return None
     return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda") -> B.KVCache:
+    """A paged 4-bit key/value cache with its device memory (left
+    uninitialised: attention looks at no place that was not appended to)."""
+    import torch
+    size = B.qkv_cache_bytes(B.KVCache(None, num_pages, page_size, kv_heads, head_dim))
+    if size == 0:
+        raise ValueError("invalid cache geometry")
+    return B.KVCache(torch.empty(size, dtype=torch.uint8, device=device), num_pages, page_size, kv_heads, head_dim)
+
+
+def attn_workspace(cache: B.KVCache, batch: int, total_q: int, max_q: int, max_kv: int, q_heads: int, device="cuda"):
+    """A workspace for qkv_attn calls of these sizes (None if none is needed)."""
+    import torch
+    n = B.qkv_attn_workspace_bytes(cache, batch, total_q, max_q, max_kv, q_heads)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def logprobs_workspace(rows: int, vocab: int, top: int, device="cuda"):
+    """A workspace for qlogprobs calls of these sizes (None if none is needed)."""
+    import torch
+    n = B.qlogprobs_workspace_bytes(rows, vocab, top)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None

@@ -2,7 +2,10 @@
  * qg.h -- C ABI of libqg: dequantize-fused low-bit weight matrix-vector
  * product (batch-1 LLM decode), its small-batch and prefill matrix-matrix
  * form, a fused greedy (argmax) output head, and the embedding-row gather
- * from the same 4-bit matrix, for AMD MI355X (gfx950).
+ * from the same 4-bit matrix, for AMD MI355X (gfx950); and the serving-step
+ * operators between those products: a paged key/value cache held in 4 bits
+ * with its page plan, append, read-back and attention, and the log
+ * probabilities of given tokens (second part of this file).
  *
  * Notation. W is M x K (M outputs, K inputs). Activations x are float32
  * [rows][K], outputs y are float32 [rows][M]; every array is row-major and
@@ -117,10 +120,11 @@ typedef enum {
 enum {
     QG_OK = 0,
     QG_ERR_NULL = -1,        /* a required pointer is NULL, or biases given where none belong */
-    QG_ERR_FORMAT = -2,      /* unknown format */
-    QG_ERR_SHAPE = -3,       /* M, K or rows out of range, or K not a multiple of the format's unit */
+    QG_ERR_FORMAT = -2,      /* unknown format or element type */
+    QG_ERR_SHAPE = -3,       /* a size, stride or count out of range or not a multiple of its unit */
     QG_ERR_ALIGN = -4,       /* a pointer is not aligned as required */
-    QG_ERR_WORKSPACE = -5,   /* ws_bytes smaller than qg_workspace_bytes(...) */
+    QG_ERR_WORKSPACE = -5,   /* ws_bytes smaller than qg_workspace_bytes(...) (or the entry
+                                point's own ..._workspace_bytes) */
     QG_ERR_ALIAS = -6,       /* a written buffer overlaps another buffer */
     QG_ERR_LAUNCH = -7,      /* the kernel launch failed */
     QG_ERR_UNSUPPORTED = -8, /* a known format this entry point does not implement
@@ -270,6 +274,198 @@ int qembed(int fmt, const void *codes, const void *scales, const void *biases,
  * keeps per-tile (value, index) pairs instead of whole logits, which is
  * what the argmax part of the workspace holds). */
 size_t qg_workspace_bytes(int op, int fmt, int64_t M, int64_t K, int64_t rows);
+
+/* ------------------------------------------------------------------------
+ * Serving-step operators
+ *
+ * One decode or prefill step of a batch of requests runs, between the
+ * products above, qkv_plan (pages and slots of the new tokens), qkv_append
+ * (their keys and values into the cache), qkv_attn (attention over the
+ * cache) and, after the output head, qlogprobs. The conventions of the top
+ * of this file hold (ownership, streams, aliasing, errors, threads);
+ * contents of device memory, such as lengths, page and slot numbers, cannot
+ * be checked on the host, so each entry point states what it makes of
+ * contents out of range. None of them reads or writes out of its buffers
+ * for any contents.
+ *
+ * The cache. Keys and values are held as the products' 4-bit weights are:
+ * groups of 64 consecutive channels of one token's head share a bf16 scale
+ * and a bf16 bias, value = scale * code + bias, code 0..15 (I Built an LLM
+ * Inference Engine on a 15 year old GPU..., "Quantization: The Model
+ * Doesn't Run on INT4": code times scale plus the minimum; Pushing the
+ * limits of legacy hardware, "Start with the machine that actually exists":
+ * group-64 codes with bf16 scale and bias). The cache is num_pages pages of
+ * page_size tokens; one page of one head is one contiguous block of
+ *
+ *     page_size * (head_dim + head_dim / 8) bytes:
+ *       K codes  uint8 [page_size][head_dim/2]   channel 2j in bits 0..3 of
+ *                                                byte j, 2j+1 in bits 4..7
+ *       K coefs  bf16  [page_size][head_dim/64][2]   (scale, bias)
+ *       V codes, V coefs   the same
+ *
+ * ordered [num_pages][kv_heads]. A slot is page * page_size + (place within
+ * the page). A whole step's cache is thus one allocation, kept resident (I
+ * Built an LLM Inference Engine..., "Optimization 3": keys and values live
+ * in preallocated memory).
+ * ------------------------------------------------------------------------ */
+
+typedef enum {
+    QG_F32 = 1,   /* float32 activations */
+    QG_BF16 = 2   /* bfloat16 activations */
+} qg_dtype;
+
+typedef struct {
+    void *data;          /* device memory, 16-byte aligned, the size above times num_pages * kv_heads */
+    int64_t num_pages;   /* >= 1; num_pages * page_size <= 2^31 - 1 */
+    int32_t page_size;   /* 16, 32, 64, 128 or 256 tokens */
+    int32_t kv_heads;    /* 1..1024 */
+    int32_t head_dim;    /* 64, 128 or 256 */
+} qg_kv_cache;
+
+/* Bytes of a cache of this geometry (data is not looked at); 0 if it is invalid. */
+size_t qkv_cache_bytes(const qg_kv_cache *cache);
+
+/*
+ * qkv_plan -- pages, lengths, row starts and slots of a step, from lengths.
+ * Request b holds len_old[b] tokens in ceil(len_old/page_size) pages, whose
+ * numbers start its row of block_table. It keeps its first keep[b] tokens
+ * (fewer after rejected speculation, 0 when it has ended) and gets n_new[b]
+ * new ones. Pages are taken from and given back to a ring of free pages:
+ * state_in = {head, tail} are running counts, entry i is
+ * ring[i mod ring_size], the free pages are entries head..tail-1.
+ *   have = ceil(len_old/page), want = ceil((keep + n_new)/page).
+ *   A request with want > have takes want - have pages from the front of the
+ *   ring, requests being served in order; it is denied if they and those of
+ *   the requests before it exceed the pages that were free before the call,
+ *   or want > table_stride. A request denied gets no page or slot and falls
+ *   back to keep[b] tokens. Pages given back (of shrinking requests, in
+ *   request order) go to the ring's end and are not taken in the same call.
+ *   block_table  int32 [batch][table_stride], entries have..want-1 of a
+ *                growing request written, all others left as they are
+ *   ring         int32 [ring_size], written at the tail; ring_size is at
+ *                least the number of pages
+ *   state_out    int64 [2], the new {head, tail}
+ *   kv_len       int32 [batch]    keep + n_new (denied: keep)
+ *   cu_q         int32 [batch+1]  running sums of n_new (denied requests
+ *                included: their rows exist and are void)
+ *   slots, pos   int32 [total]    slot and position of each new token, in
+ *                request order; slot -1 for the tokens of a denied request;
+ *                both -1 behind the last token (total may be larger, as
+ *                under graph capture; tokens behind total are dropped)
+ *   denied       int32 [1]        how many requests were denied
+ * state_in and state_out are distinct, so that a step can be planned again.
+ * Contents out of range: len_old, keep and n_new are taken into
+ * [0, 2^30], keep into [0, len_old]; a negative ring count is no free page;
+ * pages of a request behind table_stride are neither read nor given back;
+ * page numbers pass through as they are.
+ *   1 <= batch <= QG_MAX_PLAN_BATCH, 0 <= total, table_stride >= 1,
+ *   ring_size >= 1, page_size a power of two in 1..2^20.
+ */
+#define QG_MAX_PLAN_BATCH 8192
+int qkv_plan(const int32_t *len_old, const int32_t *keep, const int32_t *n_new, int batch,
+             int page_size, int32_t *block_table, int64_t table_stride, int32_t *ring,
+             int64_t ring_size, const int64_t *state_in, int64_t *state_out, int32_t *kv_len,
+             int32_t *cu_q, int32_t *slots, int32_t *pos, int64_t total, int32_t *denied,
+             hipStream_t stream);
+
+/*
+ * qkv_append -- keys and values of n tokens quantized into their slots.
+ *   k, v   [n] rows of kv_heads * head_dim elements of `dtype`, k_stride and
+ *          v_stride elements apart (parts of a fused projection's rows)
+ *   slots  int32 [n]; a token whose slot is outside the cache is skipped.
+ *          Two tokens with one slot leave either token's bytes, mixed.
+ * Each group x[0..63] is stored as
+ *   scale = bf16((max x - min x) / 15), bias = bf16(min x)   (nearest even)
+ *   code  = round_half_even((x - bias) / scale), into 0..15,
+ * in float32 arithmetic. A scale below 2^-126 is stored as 0 with codes 0
+ * (the group is its minimum); where scale or bias is not finite (a group
+ * with a NaN, an infinity, or a range past bf16) both are stored as NaN
+ * with codes 0, so that the group reads as NaN throughout.
+ *   0 <= n; strides at least kv_heads * head_dim and multiples of 16 bytes.
+ */
+int qkv_append(int dtype, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+               const int32_t *slots, int64_t n, const qg_kv_cache *cache, hipStream_t stream);
+
+/*
+ * qkv_read -- the values that n slots of the cache stand for.
+ *   k, v   [n] rows as in qkv_append, of `dtype` (written): scale * code +
+ *          bias in float32 (fused), rounded to nearest even for bfloat16.
+ *          Either may be NULL.
+ *   slots  a slot outside the cache gives a row of quiet NaNs.
+ */
+int qkv_read(int dtype, const qg_kv_cache *cache, const int32_t *slots, int64_t n, void *k,
+             int64_t k_stride, void *v, int64_t v_stride, hipStream_t stream);
+
+/*
+ * qkv_attn -- causal attention of new tokens over the cache.
+ * Request b has the query rows cu_q[b]..cu_q[b+1]-1; they are the last of
+ * its kv_len[b] tokens, whose keys and values are in the cache already (the
+ * new ones too). Row i of request b is token p = kv_len - n_q + i; head h
+ * reads key/value head h / (q_heads / kv_heads), and
+ *   out = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale * q . k_j),
+ *   lse = log sum_j w_j                (natural logarithm)
+ * over the tokens j <= p, with window > 0 only those with j > p - window.
+ * Codes enter the matrix cores exactly; float32 queries and weights as two
+ * binary16 pieces (22 bits), bfloat16 queries exactly and their weights as
+ * one; scales, softmax statistics and sums are float32. One token a request
+ * is a decode step, a few a speculation's check, many a prompt chunk: one
+ * entry point, kernels chosen by the sizes. Results do not depend on the
+ * schedule.
+ *   q, out   rows of q_heads * head_dim elements of `dtype`, q_stride and
+ *            out_stride elements apart
+ *   lse      float32 [total_q][q_heads], or NULL
+ *   block_table  int32 [batch][table_stride]
+ *   max_q    at least the longest request's rows (chooses the kernel; a
+ *            smaller value costs time, not correctness)
+ *   max_kv   at least the longest kv_len; max_kv <= table_stride * page_size
+ * A row that sees no token (kv_len 0, or fewer tokens than rows) gives out 0
+ * and lse -infinity. Contents out of range: a request with kv_len > max_kv,
+ * and rows that see a page number outside the cache, give NaN; kv_len < 0 is
+ * 0; rows outside [0, total_q) do not exist, and rows of no request are not
+ * written. What masked places hold (codes or coefficients of tokens a row
+ * does not see, NaN and infinities among them) does not matter.
+ *   1 <= batch <= 65535, 1 <= total_q <= 2^31 - 1, 1 <= max_q, 1 <= max_kv
+ *   <= 2^30, q_heads a multiple of kv_heads, q_heads <= 1024, scale finite
+ *   and > 0, window >= 0, strides as in qkv_append.
+ * Workspace: qkv_attn_workspace_bytes(...) for the same arguments (partial
+ * sums where the keys of a request are split over workgroups).
+ */
+int qkv_attn(int dtype, const void *q, int64_t q_stride, const qg_kv_cache *cache,
+             const int32_t *block_table, int64_t table_stride, const int32_t *cu_q,
+             const int32_t *kv_len, int batch, int64_t total_q, int64_t max_q, int64_t max_kv,
+             int q_heads, float scale, int64_t window, void *out, int64_t out_stride, float *lse,
+             void *ws, size_t ws_bytes, hipStream_t stream);
+size_t qkv_attn_workspace_bytes(const qg_kv_cache *cache, int batch, int64_t total_q, int64_t max_q,
+                                int64_t max_kv, int q_heads);
+
+/*
+ * qlogprobs -- log probabilities of given tokens, entropy and the best
+ * alternatives, from logits such as qgemv_argmax or qgemm writes (Pushing
+ * the limits of legacy hardware, "Build the execution path, then share the
+ * weights": greedy selection needs only the maxima; sampling, scoring and
+ * returned alternatives need the normalised distribution).
+ * With x a row and L = log sum_m exp(x[m]):
+ *   logprob[n] = x[ids[n]] - L
+ *   entropy[n] = -sum_m p[m] log p[m],  p = exp(x - L), 0 log 0 = 0
+ *   rank[n]    = 1 + how many tokens come before ids[n] in the order of
+ *                larger logits first, ties by lower index
+ *   top_ids, top_logprobs [rows][top]: the first `top` tokens of that order
+ * -0 equals +0. An id outside [0, vocab) gives logprob NaN and rank 0. A row
+ * with a NaN or +infinity, or with nothing but -infinity, has no
+ * distribution: logprob, entropy and top_logprobs are NaN; rank and top_ids
+ * are then within range but otherwise unspecified.
+ *   logits  float32, rows `ld` elements apart (ld >= vocab, 4-byte aligned)
+ *   ids     int32 [rows], or NULL (then logprob and rank must be NULL)
+ *   logprob, entropy float32 [rows], rank int32 [rows]: each may be NULL
+ *   top_ids int32, top_logprobs float32 [rows][top]; both NULL if top is 0
+ *   1 <= rows <= 2^31 - 1, 1 <= vocab <= 2^30, 0 <= top <= min(vocab,
+ *   QG_MAX_TOP). Workspace: qlogprobs_workspace_bytes(rows, vocab, top).
+ */
+#define QG_MAX_TOP 64
+int qlogprobs(const float *logits, int64_t ld, int64_t rows, int64_t vocab, const int32_t *ids, int top,
+              float *logprob, float *entropy, int32_t *rank, int32_t *top_ids, float *top_logprobs,
+              void *ws, size_t ws_bytes, hipStream_t stream);
+size_t qlogprobs_workspace_bytes(int64_t rows, int64_t vocab, int top);
 
 /* Static text for a status code. */
 const char *qg_status_str(int status);
