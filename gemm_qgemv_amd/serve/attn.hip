@@ -32,12 +32,12 @@ AttnPlan plan_attn(const qg_kv_cache &c, int batch, int64_t total_q, int64_t max
     a.rows = 16 * a.rw * a.qt;
     a.slots = total_q * group / a.rows + batch;
     const int step = qg::attn_tile_tokens(c.head_dim, a.qt) * (4 / a.rw);     // tokens of a workgroup's round of tiles
-    // enough workgroups for two on every compute unit, twice over
+    // two workgroups on every compute unit
     const int64_t tiles = std::max<int64_t>(1, total_q * group / a.rows);
     const int64_t have = std::max(tiles, std::min<int64_t>(batch, total_q)) * c.kv_heads;
-    const int64_t want = ceil_div(4 * kComputeUnits, have);
+    const int64_t want = std::max<int64_t>(1, (2 * kComputeUnits + have / 2) / have);
     const int64_t most_splits = ceil_div(max_kv, step);
-    a.nsplit = static_cast<int>(std::clamp<int64_t>(want, 1, std::min<int64_t>(most_splits, 256)));
+    a.nsplit = static_cast<int>(std::clamp<int64_t>(want, 1, std::min<int64_t>(most_splits, qg::kMaxSplits)));
     // a window's or a tile's first token is rounded down to a tile: one more
     a.chunk = static_cast<int32_t>(round_up(ceil_div(max_kv + qg::attn_tile_tokens(c.head_dim, a.qt), a.nsplit), step));
     a.nsplit = static_cast<int>(ceil_div(max_kv + qg::attn_tile_tokens(c.head_dim, a.qt), a.chunk));
@@ -68,7 +68,7 @@ int check_attn_sizes(const qg_kv_cache &c, int batch, int64_t total_q, int64_t m
         return QG_ERR_SHAPE;
     const AttnPlan a = plan_attn(c, batch, total_q, max_q, max_kv, q_heads);
     const int64_t rows = total_q * q_heads;
-    return a.slots * c.kv_heads > 0x7fffffffLL || ceil_div(rows, 4) > 0x7fffffffLL ? QG_ERR_SHAPE : QG_OK;
+    return a.slots * c.kv_heads > 0x7fffffffLL || rows > 0x7fffffffLL ? QG_ERR_SHAPE : QG_OK;
 }
 
 template <typename T, int D, int RW, int QT>
@@ -84,9 +84,14 @@ void launch_attn(const AttnPlan &a, const qg::AttnParams &p, hipStream_t s)
     (void)allowed;
     const dim3 grid(static_cast<unsigned>(a.slots * p.kv.heads), static_cast<unsigned>(a.nsplit));
     hipLaunchKernelGGL(kernel, grid, dim3(qg::kAttnThreads), lds, s, p);
-    if (a.nsplit > 1)
-        hipLaunchKernelGGL((qg::attn_join_kernel<T, D, 16 * RW * QT, qg::attn_tile_tokens(D, QT)>), dim3(static_cast<unsigned>(ceil_div(p.total_q * p.q_heads, 4))),
-                           dim3(256), 0, s, p);
+    if (a.nsplit == 1) return;
+    constexpr int TOK = qg::attn_tile_tokens(D, QT);
+    const int64_t rows = p.total_q * p.q_heads;
+    if (a.nsplit <= 16)
+        hipLaunchKernelGGL((qg::attn_join_kernel<T, D, 16 * RW * QT, TOK, 1>), dim3(static_cast<unsigned>(ceil_div(rows, 4))), dim3(256),
+                           0, s, p);
+    else
+        hipLaunchKernelGGL((qg::attn_join_kernel<T, D, 16 * RW * QT, TOK, 4>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, p);
 }
 
 template <typename T, int D>

@@ -151,17 +151,23 @@ __device__ __forceinline__ f16x8 nibbles_tiny(uint32_t w)
     return __builtin_bit_cast(f16x8, r);
 }
 
+// Masks and the bits of 1024 in registers: an AND and an OR with two literals
+// would not go into one instruction.
+struct NibbleBits {
+    uint32_t even = 0x000f000fu, odd = 0x00f000f0u, thousand = 0x64006400u;
+    __device__ NibbleBits() { asm("" : "+s"(even), "+s"(odd), "+v"(thousand)); }
+};
+
 // Eight nibbles as c - 8: halves (0,4), (1,5)*16, (2,6), (3,7)*16. With the
 // bits of 1024 set, a half is 1024 + nibble (or + 16 nibble) exactly.
-__device__ __forceinline__ f16x8 nibbles_centred(uint32_t w)
+__device__ __forceinline__ f16x8 nibbles_centred(uint32_t w, const NibbleBits &k)
 {
     const uint32_t v = w >> 8;
     const f16x2 even = {(_Float16)-1032.0f, (_Float16)-1032.0f}, odd = {(_Float16)-1152.0f, (_Float16)-1152.0f};
-    auto put = [](uint32_t x, f16x2 off) {
-        return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, x | 0x64006400u) + off);
+    auto put = [&](uint32_t x, uint32_t mask, f16x2 off) {
+        return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, (x & mask) | k.thousand) + off);
     };
-    const u32x4 r = {put(w & 0x000f000fu, even), put(w & 0x00f000f0u, odd), put(v & 0x000f000fu, even),
-                     put(v & 0x00f000f0u, odd)};
+    const u32x4 r = {put(w, k.even, even), put(w, k.odd, odd), put(v, k.even, even), put(v, k.odd, odd)};
     return __builtin_bit_cast(f16x8, r);
 }
 
@@ -174,6 +180,17 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b)
     // of float32 for the pair, and one of some 8000 pairs differs.
     asm("" : "+v"(v));
     return v;
+}
+
+// A dword of codes as an operand. With float32 queries the codes are centred;
+// the matrix cores take subnormals, but keep fewer bits of sums of their
+// products (scores 5 times, outputs 8 times as far from the exact ones), which
+// bfloat16's own rounding covers, at 5 instead of 9 instructions a dword.
+template <bool CENTRED>
+__device__ __forceinline__ f16x8 nibbles(uint32_t w, const NibbleBits &k)
+{
+    if constexpr (CENTRED) return nibbles_centred(w, k);
+    else return nibbles_tiny(w);
 }
 
 // Maximum (NaN ignored) over the four lanes that share l % 16.
@@ -204,10 +221,9 @@ template <int D, int TOK>
 struct TileLds {
     static constexpr int kTok = TOK;
     static constexpr int kRow = D / 2;                     // code bytes of a token
-    uint8_t k[kTok * kRow];
-    uint8_t v[kTok * kRow];
-    float kco[D / 64][2][kTok];                            // scale, bias
-    float vco[D / 64][2][kTok];                            // scale (odd tokens: / 16), bias + 8 scale
+    uint8_t codes[2 * kTok * kRow];                        // K, V
+    // scale (V, odd tokens: / 16) and bias (float32 queries: + 8 scale) of K, V
+    float co[2][D / 64][2][kTok];
     float top[4];                                          // largest |value scale| of a staging wave
 };
 
@@ -242,13 +258,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(AttnParams p)
     static_assert(RW * KW * 64 == kAttnThreads, "four waves");
     constexpr bool kTwo = sizeof(T) == 4;                  // float32: two pieces
     constexpr int kTok = attn_tile_tokens(D, QT), NA = kTok / 16, NST = kTok / 32, NG = D / 64;
+    constexpr float kUnit = kTwo ? 1.0f : 5.9604644775390625e-08f;       // of a code as the matrix cores see it
     constexpr int R = 16 * QT * RW;                        // query rows of the workgroup
-    constexpr int NT = RW * 64;                            // threads that fetch a tile
     constexpr int kRow = D / 2, kSeg = kRow / 16;          // code bytes, 16-byte granules of a token
-    constexpr int kGran = kTok * kSeg;                     // granules of K (and of V) in a tile
-    constexpr int NL = 2 * kGran / NT;                     // granules a thread fetches
-    constexpr int NP = NT <= kGran ? NL / 2 : NL;          // distinct tokens among them
-    constexpr int NC = 2 * kTok > NT ? 2 * kTok / NT : 1;  // tokens whose coefficients a thread fetches
     extern __shared__ __align__(16) uint8_t lds[];
 
     // the lane number is made opaque anew in every round of tiles: the many
@@ -257,7 +269,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(AttnParams p)
     int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rw = wave % RW, kw = wave / RW;
-    int col = lane & 15, g4 = lane >> 4, tid = rw * 64 + lane;
+    int col = lane & 15, g4 = lane >> 4;
     const int kv_head = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.kv.heads));
     RowTile t;
     if (!find_tile<R>(p, blockIdx.x / static_cast<unsigned>(p.kv.heads), t)) return;
@@ -300,8 +312,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(AttnParams p)
         int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xff);
         e = e < 40 ? 40 : e > 240 ? 240 : e;
         const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 + 127 - e) << 23);
-        // scores come out as (q * up) . (code * 2^-24)
-        factor[qt] = p.scale_log2e * __uint_as_float(static_cast<uint32_t>(127 - 13 - 127 + e) << 23);
+        // scores come out as (q * up) . (code * kUnit)
+        factor[qt] = p.scale_log2e / kUnit * __uint_as_float(static_cast<uint32_t>(127 - 13 - 127 + e) << 23);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             float sum = 0.0f;
@@ -322,7 +334,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(AttnParams p)
                 if constexpr (kTwo) ql[qt][g][st] = __builtin_bit_cast(f16x8, l);
             }
             sum = pair_sum<5>(pair_sum<4>(sum));
-            qsum[qt][g] = sum;
+            qsum[qt][g] = sum * kUnit;
         }
     }
 
@@ -345,82 +357,86 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(AttnParams p)
     using Tile = TileLds<D, kTok>;
     Tile *const bufs = reinterpret_cast<Tile *>(lds) + kw * (RW > 1 ? 2 : 1);
 
-    // token (within the tile) of granule n of this thread, and of its coefficients
-    auto gran_token = [&](int n) { return ((n * NT + tid) % kGran) / kSeg; };
-    auto coef_token = [&](int n) { return (n * NT + tid) % kTok; };
-    int32_t pid[NP], cpid;
+    // A tile comes in blocks of 16 tokens (a page holds whole blocks), which a
+    // wave reads as contiguous pieces: the block's address is scalar, a lane's
+    // offset constant. The waves of a group take blocks in turn; with more
+    // waves than blocks K and V of a block go to two of them.
+    constexpr int NB = kTok / 16, NBW = RW < NB ? NB / RW : 1;
+    constexpr bool kHalves = RW > NB;
+    constexpr int kPieces = D == 64 ? 1 : (kHalves ? 1 : 2) * (D / 128);     // 16-byte loads a lane makes for a block
+    const int my_block = rw % NB, my_part = kHalves ? rw / NB : 0;
+    const int64_t half = p.kv.block_bytes >> 1;
+    // part (K 0, V 1), token in the block and granule of a lane's piece n
+    auto piece_part = [&](int n) { return D == 64 ? lane >> 5 : kHalves ? my_part : n / (D / 128); };
+    auto piece_token = [&](int n) { return D == 64 ? (lane & 31) >> 1 : (n % (D / 128)) * (64 / kSeg) + lane / kSeg; };
+    int32_t page_ids;                                       // lane j: the page of block j (mod NB)
     auto fetch_pages = [&](int tile) {
-        const int32_t base = begin + tile * kTok;
-        auto page_of = [&](int tok) {
-            const int32_t at = base + tok < end ? base + tok : end - 1;
-            return row_pages[at >> p.kv.page_shift];
-        };
-#pragma unroll
-        for (int n = 0; n < NP; ++n) pid[n] = page_of(gran_token(n));
-        cpid = page_of(coef_token(0));
+        const int32_t want = begin + tile * kTok + (lane & (NB - 1)) * 16;
+        page_ids = row_pages[(want < end ? want : end - 1) >> p.kv.page_shift];
     };
-    u32x4 code[NL];
-    uint32_t coef[NC][NG] = {};
+    u32x4 code[NBW][kPieces];
+    uint32_t coef[NBW][NG];                                 // lane: part (lane / 16) % 2, token lane % 16
     auto fetch_tile = [&](int tile) {
         const int32_t base = begin + tile * kTok;
 #pragma unroll
-        for (int n = 0; n < NL; ++n) {
-            const int idx = n * NT + tid, part = idx / kGran, tok = gran_token(n), seg = idx % kSeg;
-            const int32_t id = pid[n % NP];
-            const int64_t page = id >= 0 && id < p.kv.num_pages ? id : 0;
-            const int at = (base + tok) & page_mask;
-            code[n] = *reinterpret_cast<const u32x4 *>(p.kv.data + page * p.kv.page_bytes + head_off +
-                                                       kv_part(p.kv, part) + at * kRow + seg * 16);
-        }
-        const bool known = cpid >= 0 && cpid < p.kv.num_pages;
-        const int64_t page = known ? cpid : 0;
+        for (int j = 0; j < NBW; ++j) {
+            const int blk = my_block + j * RW;
+            const int32_t id = __builtin_amdgcn_readlane(page_ids, blk);
+            const bool known = id >= 0 && id < p.kv.num_pages;
+            const uint8_t *page = p.kv.data + (known ? id : 0) * p.kv.page_bytes + head_off;
+            const int at = (base + blk * 16) & page_mask;
+            const uint8_t *src = page + at * kRow;
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            const int idx = n * NT + tid, part = idx / kTok, tok = coef_token(n);
-            const int at = (base + tok) & page_mask;
-            if (NT <= 2 * kTok || idx < 2 * kTok) {
-                const uint8_t *src = p.kv.data + page * p.kv.page_bytes + head_off + kv_coefs(p.kv, part) + at * (D / 16);
-                if constexpr (NG == 1) {
-                    coef[n][0] = *reinterpret_cast<const uint32_t *>(src);
-                } else if constexpr (NG == 2) {
-                    const u32x2 v = *reinterpret_cast<const u32x2 *>(src);
-                    coef[n][0] = v[0], coef[n][1] = v[1];
-                } else {
-                    const u32x4 v = *reinterpret_cast<const u32x4 *>(src);
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) coef[n][g] = v[g];
-                }
+            for (int n = 0; n < kPieces; ++n) {
+                if constexpr (D == 64)
+                    code[j][n] = *reinterpret_cast<const u32x4 *>(src + static_cast<uint32_t>((lane >> 5) * half + (lane & 31) * 16));
+                else
+                    code[j][n] = *reinterpret_cast<const u32x4 *>(src + piece_part(n) * half + (n % (D / 128)) * 1024 +
+                                                                  static_cast<uint32_t>(lane * 16));
             }
+            if (!kHalves || my_part == 0) {
+                const uint8_t *co = page + ((D / 2) << p.kv.page_shift) + at * (D / 16) +
+                                    static_cast<uint32_t>(((lane >> 4) & 1) * half + (lane & 15) * (D / 16));
+                if constexpr (NG == 1) {
+                    coef[j][0] = *reinterpret_cast<const uint32_t *>(co);
+                } else if constexpr (NG == 2) {
+                    const u32x2 v = *reinterpret_cast<const u32x2 *>(co);
+                    coef[j][0] = v[0], coef[j][1] = v[1];
+                } else {
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(co);
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                if (!known) coef[n][g] = 0x7fc07fc0u;                     // a page outside the cache reads as NaN
-                if (base + tok >= end) coef[n][g] = 0;                    // what lies behind the last token is not looked at
+                    for (int g = 0; g < NG; ++g) coef[j][g] = v[g];
+                }
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    if (!known) coef[j][g] = 0x7fc07fc0u;                              // a page outside the cache reads as NaN
+                    if (base + blk * 16 + (lane & 15) >= end) coef[j][g] = 0;          // places behind the last token hold anything
+                }
             }
         }
     };
     // the fetched tile into LDS; returns the largest |value scale| this wave saw
     auto put_tile = [&](Tile &s) {
         float top = 0.0f;
+        const bool is_v = (lane >> 4) & 1;
+        const float odd = is_v && (lane & 1) ? 0.0625f : 1.0f;
 #pragma unroll
-        for (int n = 0; n < NL; ++n) {
-            const int idx = n * NT + tid, part = idx / kGran, tok = gran_token(n), seg = idx % kSeg;
-            const int to = part == 0 ? seg ^ k_swizzle<D>(tok) : seg ^ v_swizzle<D>(tok);
-            *reinterpret_cast<u32x4 *>((part == 0 ? s.k : s.v) + tok * kRow + to * 16) = code[n];
-        }
+        for (int j = 0; j < NBW; ++j) {
+            const int blk = my_block + j * RW;
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            const int idx = n * NT + tid, part = idx / kTok, tok = coef_token(n);
-            if (NT <= 2 * kTok || idx < 2 * kTok) {
+            for (int n = 0; n < kPieces; ++n) {
+                const int part = piece_part(n), tok = blk * 16 + piece_token(n), seg = lane % kSeg;
+                const int to = seg ^ (part == 0 ? k_swizzle<D>(tok) : v_swizzle<D>(tok));
+                *reinterpret_cast<u32x4 *>(s.codes + (part * kTok + tok) * kRow + to * 16) = code[j][n];
+            }
+            if (!kHalves || my_part == 0) {
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    const float sc = __uint_as_float(coef[n][g] << 16), bi = __uint_as_float(coef[n][g] & 0xffff0000u);
-                    if (part == 0) {
-                        s.kco[g][0][tok] = sc;
-                        s.kco[g][1][tok] = fmaf(8.0f, sc, bi);
-                    } else {
-                        top = fmaxf(top, fabsf(sc));
-                        s.vco[g][0][tok] = tok & 1 ? sc * 0.0625f : sc;
-                        s.vco[g][1][tok] = fmaf(8.0f, sc, bi);
+                    const float sc = __uint_as_float(coef[j][g] << 16), bi = __uint_as_float(coef[j][g] & 0xffff0000u);
+                    top = fmaxf(top, fabsf(sc));
+                    if (lane < 32) {
+                        s.co[is_v][g][0][blk * 16 + (lane & 15)] = sc * odd;
+                        s.co[is_v][g][1][blk * 16 + (lane & 15)] = kTwo ? fmaf(8.0f, sc, bi) : bi;
                     }
                 }
             }
@@ -429,25 +445,24 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(AttnParams p)
         top = fmaxf(top, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(top), 0x4E, 0xF, 0xF, false)));
         top = fmaxf(top, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(top), 0x124, 0xF, 0xF, false)));
         top = fmaxf(top, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(top), 0x128, 0xF, 0xF, false)));
-        return max_over_groups(top);
+        return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(top), 16));     // the lanes of V
     };
 
+    const NibbleBits bits;
     // ---- one tile -------------------------------------------------------------
     auto compute = [&](const Tile &s, float top, int32_t base, auto masked_tag) {
         constexpr bool kMasked = decltype(masked_tag)::value;
         f32x4 x[QT][NA];
 #pragma unroll
         for (int a = 0; a < NA; ++a) {
-            __builtin_amdgcn_sched_barrier(0);
             const int tok = a * 16 + col;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                if constexpr (D * QT >= 256) __builtin_amdgcn_sched_barrier(0);
                 const int seg = (g * 2 + (g4 >> 1)) ^ k_swizzle<D>(tok);
-                const u32x2 w = *reinterpret_cast<const u32x2 *>(s.k + tok * kRow + seg * 16 + (g4 & 1) * 8);
-                const f16x8 k0 = nibbles_centred(w[0]), k1 = nibbles_centred(w[1]);
-                const f32x4 sc = *reinterpret_cast<const f32x4 *>(&s.kco[g][0][a * 16 + g4 * 4]);
-                const f32x4 bi = *reinterpret_cast<const f32x4 *>(&s.kco[g][1][a * 16 + g4 * 4]);
+                const u32x2 w = *reinterpret_cast<const u32x2 *>(s.codes + tok * kRow + seg * 16 + (g4 & 1) * 8);
+                const f16x8 k0 = nibbles<kTwo>(w[0], bits), k1 = nibbles<kTwo>(w[1], bits);
+                const f32x4 sc = *reinterpret_cast<const f32x4 *>(&s.co[0][g][0][a * 16 + g4 * 4]);
+                const f32x4 bi = *reinterpret_cast<const f32x4 *>(&s.co[0][g][1][a * 16 + g4 * 4]);
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt) {
                     f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -485,7 +500,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(AttnParams p)
                     f32x4 sc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
-                        const f32x4 v = *reinterpret_cast<const f32x4 *>(&s.vco[g][0][a * 16 + g4 * 4]);
+                        const f32x4 v = *reinterpret_cast<const f32x4 *>(&s.co[1][g][0][a * 16 + g4 * 4]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) sc[i] = fmaxf(sc[i], fabsf(v[i]) * (i & 1 ? 16.0f : 1.0f));
                     }
@@ -534,15 +549,15 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(AttnParams p)
         // out += V^T w
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_sched_barrier(0);               // or the operands of several groups are held at once
             f16x8 ph[QT][NST], pl[kTwo ? QT : 1][NST];
 #pragma unroll
             for (int st = 0; st < NST; ++st) {
                 f32x4 sc[2], bi[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    sc[h] = *reinterpret_cast<const f32x4 *>(&s.vco[g][0][(st * 2 + h) * 16 + g4 * 4]);
-                    bi[h] = *reinterpret_cast<const f32x4 *>(&s.vco[g][1][(st * 2 + h) * 16 + g4 * 4]);
+                    sc[h] = *reinterpret_cast<const f32x4 *>(&s.co[1][g][0][(st * 2 + h) * 16 + g4 * 4]);
+                    bi[h] = *reinterpret_cast<const f32x4 *>(&s.co[1][g][1][(st * 2 + h) * 16 + g4 * 4]);
                 }
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt) {
@@ -578,7 +593,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(AttnParams p)
             auto transposed = [&](int chunk, int tok) {     // chunk: 8-byte piece of the token's codes
                 const int seg = (chunk >> 1) ^ v_swizzle<D>(tok);
                 return __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-                    (LdsPtr)(__attribute__((address_space(3))) void *)(s.v + tok * kRow + seg * 16 + (chunk & 1) * 8));
+                    (LdsPtr)(__attribute__((address_space(3))) void *)(s.codes + (kTok + tok) * kRow + seg * 16 + (chunk & 1) * 8));
             };
             if constexpr (kTok == 64) {
                 const int tok = (col >> 2) * 16 + g4 * 4 + (col & 3);
@@ -587,7 +602,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(AttnParams p)
                     const i32x2 w = transposed(g * 4 + db, tok);
 #pragma unroll
                     for (int st = 0; st < NST; ++st) {
-                        const f16x8 v = nibbles_centred(static_cast<uint32_t>(w[st]));
+                        const f16x8 v = nibbles<kTwo>(static_cast<uint32_t>(w[st]), bits);
 #pragma unroll
                         for (int qt = 0; qt < QT; ++qt) {
                             acc[qt][g * 4 + db] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, ph[qt][st], acc[qt][g * 4 + db], 0, 0, 0);
@@ -603,7 +618,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(AttnParams p)
                     const i32x2 w = transposed(g * 4 + dp * 2 + (col >> 3), tok);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const f16x8 v = nibbles_centred(static_cast<uint32_t>(w[h]));
+                        const f16x8 v = nibbles<kTwo>(static_cast<uint32_t>(w[h]), bits);
                         const int db = g * 4 + dp * 2 + h;
 #pragma unroll
                         for (int qt = 0; qt < QT; ++qt) {
@@ -635,12 +650,12 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(AttnParams p)
         const int tile = kw + i * KW;
         const bool live = tile < tiles;
         asm volatile("" : "+v"(lane));
-        col = lane & 15, g4 = lane >> 4, tid = rw * 64 + lane;
+        col = lane & 15, g4 = lane >> 4;
         Tile &s = bufs[RW > 1 ? i & 1 : 0];
         float top = 0.0f;
         if (live) top = put_tile(s);
         if constexpr (RW > 1) {
-            if (live && lane == 0) s.top[rw] = top;
+            if (live && lane == 0) s.top[rw] = top;      // 0 from waves that fetch no coefficients
             __syncthreads();
         } else {
             // one wave's LDS operations complete in order; keep the compiler from moving them
@@ -673,7 +688,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(AttnParams p)
         for (int g = 0; g < NG; ++g) {
             const float b = pair_sum<5>(pair_sum<4>(bias[qt][g]));
 #pragma unroll
-            for (int db = 0; db < 4; ++db) acc[qt][g * 4 + db] += b;
+            for (int db = 0; db < 4; ++db) {
+                acc[qt][g * 4 + db] *= 1.0f / kUnit;
+                acc[qt][g * 4 + db] += b;
+            }
         }
     }
     const float nan = __builtin_nanf("");
@@ -754,17 +772,25 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_kernel(AttnParams p)
     }
 }
 
-// Joins the splits of one row and head: a wave each, lanes over the
-// channels. The rows of a tile share their splits, so their count is found
+// Joins the splits of a row and head: WAVES waves of a workgroup of 4 each
+// (one where splits are few, four where rows are few and splits many). The
+// statistics of the splits are taken a lane each; then runs of D / 4 lanes
+// add up the splits s = run, run + runs, ..., and the runs are added in a
+// fixed tree. The rows of a tile share their splits, so their count is found
 // from the row's tile as attn_kernel does.
-template <typename T, int D, int R, int TOK>
+constexpr int kMaxSplits = 256;
+
+template <typename T, int D, int R, int TOK, int WAVES>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p)
 {
-    constexpr int kTok = TOK;
-    constexpr int kPer = D / 64;
-    const int lane = threadIdx.x & 63;
-    const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    if (row >= p.total_q * p.q_heads) return;
+    constexpr int kLanes = D / 4, kRuns = WAVES * 64 / kLanes;
+    __shared__ float weight[4 / WAVES][WAVES == 1 ? 64 : kMaxSplits];
+    __shared__ f32x4 sums[WAVES == 1 ? 1 : 4][kLanes];
+    __shared__ float red[4][2];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int mine = WAVES == 1 ? wave : 0, id = WAVES == 1 ? lane : threadIdx.x;
+    const int64_t row = int64_t(blockIdx.x) * (4 / WAVES) + mine;
+    if (row >= p.total_q * p.q_heads) return;              // whole waves; never with WAVES = 4
     const int64_t tok = row / p.q_heads;
     const int head = static_cast<int>(row - tok * p.q_heads);
     // the request of this query row: the last that starts at or before it
@@ -783,34 +809,70 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p)
     if (tok - t.q0 >= t.n_q) return;
     const int64_t r = (tok - t.q0) * p.group + head % p.group;
     tile_tokens(p, t, r / R * R, R);
-    const int32_t from = t.lo / kTok * kTok;
+    const int32_t from = t.lo / TOK * TOK;
     int n = static_cast<int>((int64_t(t.hi) - from + p.chunk - 1) / p.chunk);
     n = t.hi <= from ? 0 : n < p.nsplit ? n : p.nsplit;
 
     const float *stat = p.part_stat + row * p.nsplit * 2;
-    const float *part = p.part_out + row * p.nsplit * D + lane * kPer;
-    float m = kNoReference, sum = 0.0f, o[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = 0.0f;
-    for (int s = 0; s < n; ++s) {
-        const float rf = stat[s * 2];
-        m = rf > m || rf != rf ? rf : m;
+    float m = kNoReference, own = 0.0f;
+    bool bad = false;                                      // a NaN reference
+    if (id < n) {
+        m = stat[id * 2];
+        own = stat[id * 2 + 1];
+        bad = m != m;
     }
-    for (int s = 0; s < n; ++s) {
-        const float f = __builtin_amdgcn_exp2f(stat[s * 2] - m);
-        sum = fmaf(f, stat[s * 2 + 1], sum);
+    const float ref_own = m;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) o[i] = fmaf(f, part[int64_t(s) * D + i], o[i]);
+    for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, lane_xor_f32(m, d));
+    bad = __any(bad);
+    if constexpr (WAVES > 1) {
+        if (lane == 0) red[wave][0] = bad ? __builtin_nanf("") : m;
+        __syncthreads();
+        m = kNoReference;
+        bad = false;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float v = red[w][0];
+            bad = bad || v != v;
+            m = fmaxf(m, v);
+        }
+    }
+    if (bad) m = __builtin_nanf("");
+    const float f = id < n ? __builtin_amdgcn_exp2f(ref_own - m) : 0.0f;
+    float sum = f * own;
+    if (id < n) weight[mine][id] = f;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) sum += lane_xor_f32(sum, d);
+    if constexpr (WAVES > 1) {
+        if (lane == 0) red[wave][1] = sum;
+        __syncthreads();
+        sum = (red[0][1] + red[1][1]) + (red[2][1] + red[3][1]);
+    } else {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+
+    const int run = id / kLanes, quad = id % kLanes;
+    const float *part = p.part_out + row * p.nsplit * D + quad * 4;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int s = run; s < n; s += kRuns) o += weight[mine][s] * *reinterpret_cast<const f32x4 *>(part + int64_t(s) * D);
+#pragma unroll
+    for (int d = 32; d >= kLanes; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += lane_xor_f32(o[i], d);
+    if constexpr (WAVES > 1) {
+        if (lane < kLanes) sums[wave][lane] = o;
+        __syncthreads();
+        if (threadIdx.x >= kLanes) return;
+        o = (sums[0][quad] + sums[1][quad]) + (sums[2][quad] + sums[3][quad]);
+    } else if (lane >= kLanes) {
+        return;
     }
     const float nan = __builtin_nanf("");
     const float inv = t.poison ? nan : sum == 0.0f ? 0.0f : 1.0f / sum;
-    T *dst = static_cast<T *>(p.out) + tok * p.out_stride + int64_t(head) * D + lane * kPer;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        if constexpr (sizeof(T) == 4) dst[i] = o[i] * inv;
-        else dst[i] = static_cast<uint16_t>(f32_to_bf16_bits(o[i] * inv));
-    }
-    if (p.lse && lane == 0)
+    store_out4(static_cast<T *>(p.out) + tok * p.out_stride + int64_t(head) * D + quad * 4, o * inv);
+    if (p.lse && quad == 0)
         p.lse[row] = t.poison ? nan : sum == 0.0f ? -__builtin_inff() : (m + __log2f(sum)) * 0.693147180559945309f;
 }
 
