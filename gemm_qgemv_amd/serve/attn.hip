@@ -6,52 +6,53 @@
 
 #include <algorithm>
 
-#include "attn.hpp"
+#include "attn_few.hpp"
+#include "attn_join.hpp"
+#include "attn_rows.hpp"
 
 namespace {
 
 // A call's launch geometry: a pure function of sizes known on the host.
 struct AttnPlan {
-    int rows;              // query rows of a workgroup
-    int rw, qt;            // row groups of waves, 16-row tiles a wave
+    int rows;              // query rows of a workgroup: 16 or 32 (attn_few_kernel), 64 or 128 (attn_rows_kernel)
     int64_t slots;         // tile slots
+    int tile, step;        // tokens of a tile, and of a workgroup's round of tiles
     int nsplit;
     int32_t chunk;
 };
 
-// Row groups: decode steps (up to 16 rows a request and key/value head) give
-// all four waves to the tokens; the more rows, the more waves take rows, so
-// that a fetched tile serves all of them.
+constexpr int few_or_rows_tile(int dim, int rows)
+{
+    return rows <= 32 ? qg::few_tile_tokens(dim) : qg::rows_tile_tokens(dim);
+}
+
 AttnPlan plan_attn(const qg_kv_cache &c, int batch, int64_t total_q, int64_t max_q, int64_t max_kv, int q_heads)
 {
     const int group = q_heads / c.kv_heads;
     const int64_t most = std::min(max_q, total_q) * group;
     AttnPlan a;
-    a.rw = most <= 16 ? 1 : most <= 32 ? 2 : 4;
-    a.qt = most > 64 && c.head_dim <= 128 ? 2 : 1;
-    a.rows = 16 * a.rw * a.qt;
+    a.rows = most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 || c.head_dim == 256 ? 64 : 128;
     a.slots = total_q * group / a.rows + batch;
-    const int step = qg::attn_tile_tokens(c.head_dim, a.qt) * (4 / a.rw);     // tokens of a workgroup's round of tiles
+    a.tile = few_or_rows_tile(c.head_dim, a.rows);
+    a.step = a.tile * (a.rows == 16 ? 4 : a.rows == 32 ? 2 : 1);
     // two workgroups on every compute unit
     const int64_t tiles = std::max<int64_t>(1, total_q * group / a.rows);
     const int64_t have = std::max(tiles, std::min<int64_t>(batch, total_q)) * c.kv_heads;
     const int64_t want = std::max<int64_t>(1, (2 * kComputeUnits + have / 2) / have);
-    const int64_t most_splits = ceil_div(max_kv, step);
-    a.nsplit = static_cast<int>(std::clamp<int64_t>(want, 1, std::min<int64_t>(most_splits, qg::kMaxSplits)));
-    // a window's or a tile's first token is rounded down to a tile: one more
-    a.chunk = static_cast<int32_t>(round_up(ceil_div(max_kv + qg::attn_tile_tokens(c.head_dim, a.qt), a.nsplit), step));
-    a.nsplit = static_cast<int>(ceil_div(max_kv + qg::attn_tile_tokens(c.head_dim, a.qt), a.chunk));
+    a.nsplit = static_cast<int>(std::clamp<int64_t>(want, 1, std::min<int64_t>(ceil_div(max_kv, a.step), qg::kMaxSplits)));
+    // a tile's first token is rounded down to a tile: one more
+    a.chunk = static_cast<int32_t>(round_up(ceil_div(max_kv + a.tile, a.nsplit), a.step));
+    a.nsplit = static_cast<int>(ceil_div(max_kv + a.tile, a.chunk));
     return a;
 }
 
 // With a window a tile of rows sees at most window + rows tokens: as many
 // splits, of fewer tokens.
-void narrow_plan(AttnPlan &a, const qg_kv_cache &c, int64_t max_kv, int64_t window)
+void narrow_plan(AttnPlan &a, int64_t max_kv, int64_t window)
 {
     if (window >= max_kv) return;
-    const int tile = qg::attn_tile_tokens(c.head_dim, a.qt), step = tile * (4 / a.rw);
-    const int64_t range = std::min<int64_t>(max_kv, window + a.rows) + tile;
-    a.chunk = static_cast<int32_t>(round_up(ceil_div(range, a.nsplit), step));
+    const int64_t range = std::min<int64_t>(max_kv, window + a.rows) + a.tile;
+    a.chunk = static_cast<int32_t>(round_up(ceil_div(range, a.nsplit), a.step));
     a.nsplit = static_cast<int>(ceil_div(range, a.chunk));
 }
 
@@ -71,36 +72,39 @@ int check_attn_sizes(const qg_kv_cache &c, int batch, int64_t total_q, int64_t m
     return a.slots * c.kv_heads > 0x7fffffffLL || rows > 0x7fffffffLL ? QG_ERR_SHAPE : QG_OK;
 }
 
-template <typename T, int D, int RW, int QT>
-void launch_attn(const AttnPlan &a, const qg::AttnParams &p, hipStream_t s)
+template <auto KERNEL>
+void launch_with_lds(size_t lds, dim3 grid, const qg::AttnParams &p, hipStream_t s)
 {
-    constexpr int KW = 4 / RW;
-    constexpr int lds = qg::attn_lds_bytes<D, RW, KW, QT>();
-    auto kernel = qg::attn_kernel<T, D, RW, KW, QT>;
     static const bool allowed = [&] {
-        return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds) ==
-               hipSuccess;
+        return hipFuncSetAttribute(reinterpret_cast<const void *>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                   static_cast<int>(lds)) == hipSuccess;
     }();
     (void)allowed;
+    hipLaunchKernelGGL(KERNEL, grid, dim3(qg::kAttnThreads), lds, s, p);
+}
+
+template <typename T, int D, int R>
+void launch_attn(const AttnPlan &a, const qg::AttnParams &p, hipStream_t s)
+{
     const dim3 grid(static_cast<unsigned>(a.slots * p.kv.heads), static_cast<unsigned>(a.nsplit));
-    hipLaunchKernelGGL(kernel, grid, dim3(qg::kAttnThreads), lds, s, p);
+    if constexpr (R <= 32) launch_with_lds<qg::attn_few_kernel<T, D, R / 16>>(qg::few_lds_bytes<D>(), grid, p, s);
+    else launch_with_lds<qg::attn_rows_kernel<T, D, R / 64>>(sizeof(qg::RowsLds<D>), grid, p, s);
     if (a.nsplit == 1) return;
-    constexpr int TOK = qg::attn_tile_tokens(D, QT);
+    constexpr int TOK = few_or_rows_tile(D, R);
     const int64_t rows = p.total_q * p.q_heads;
     if (a.nsplit <= 16)
-        hipLaunchKernelGGL((qg::attn_join_kernel<T, D, 16 * RW * QT, TOK, 1>), dim3(static_cast<unsigned>(ceil_div(rows, 4))), dim3(256),
-                           0, s, p);
+        hipLaunchKernelGGL((qg::attn_join_kernel<T, D, R, TOK, 1>), dim3(static_cast<unsigned>(ceil_div(rows, 4))), dim3(256), 0, s, p);
     else
-        hipLaunchKernelGGL((qg::attn_join_kernel<T, D, 16 * RW * QT, TOK, 4>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, p);
+        hipLaunchKernelGGL((qg::attn_join_kernel<T, D, R, TOK, 4>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, p);
 }
 
 template <typename T, int D>
 void launch_attn_dim(const AttnPlan &a, const qg::AttnParams &p, hipStream_t s)
 {
-    if (a.rw == 1) launch_attn<T, D, 1, 1>(a, p, s);
-    else if (a.rw == 2) launch_attn<T, D, 2, 1>(a, p, s);
-    else if (a.qt == 1) launch_attn<T, D, 4, 1>(a, p, s);
-    else if constexpr (D <= 128) launch_attn<T, D, 4, 2>(a, p, s);
+    if (a.rows == 16) launch_attn<T, D, 16>(a, p, s);
+    else if (a.rows == 32) launch_attn<T, D, 32>(a, p, s);
+    else if (a.rows == 64) launch_attn<T, D, 64>(a, p, s);
+    else if constexpr (D <= 128) launch_attn<T, D, 128>(a, p, s);
 }
 
 template <typename T>
@@ -145,7 +149,7 @@ int qkv_attn(int dtype, const void *q, int64_t q_stride, const qg_kv_cache *cach
         !aligned(kv_len, 4) || (lse && !aligned(lse, 4)))
         return QG_ERR_ALIGN;
     AttnPlan a = plan_attn(*cache, batch, total_q, max_q, max_kv, q_heads);
-    if (window > 0) narrow_plan(a, *cache, max_kv, window);
+    if (window > 0) narrow_plan(a, max_kv, window);
     const size_t need = attn_workspace(a, *cache, total_q, q_heads);
     if (need > 0) {
         if (!ws || ws_bytes < need) return QG_ERR_WORKSPACE;
@@ -176,7 +180,7 @@ int qkv_attn(int dtype, const void *q, int64_t q_stride, const qg_kv_cache *cach
     p.group = q_heads / cache->kv_heads;
     p.q_heads = q_heads;
     p.scale_log2e = scale * 1.44269504088896340736f;
-    p.window = window > max_kv ? 0 : window;
+    p.window = window > max_kv ? 0 : static_cast<int32_t>(window);
     p.out = out;
     p.out_stride = out_stride;
     p.lse = lse;

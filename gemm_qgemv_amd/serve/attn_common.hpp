@@ -1,0 +1,537 @@
+// attn_common.hpp -- causal attention of new tokens over the paged 4-bit cache.
+//
+// Mathematics. For a query row q and tokens t with key k_t[d] =
+// s_t[g] * c_t[d] + b_t[g] (g = d / 64, c the 4-bit code),
+//
+//   x_t = q . k_t = sum_g ( s_t[g] * sum_{d in g} q[d] c_t[d] + b_t[g] * Q[g] ),   Q[g] = sum_{d in g} q[d],
+//   out[d] = ( sum_t (w_t s'_t[g]) (c'_t[d] - 8) + sum_t w_t (b'_t[g] + 8 s'_t[g]) ) / sum_t w_t,   w_t = 2^(f x_t - R),
+//
+// one pass over the tokens with a reference R a row (the softmax does not
+// depend on R). The codes themselves go to the matrix cores: they are exact
+// in binary16, so nothing of the cache is rounded, and a float32 query or
+// weight goes as two binary16 pieces (22 bits) where a dequantized cache
+// would need three products of pieces. Scales and biases are applied in
+// float32 outside of them. The value codes are centred (c - 8) so that the
+// accumulators hold sums that cancel no worse than the result does.
+//
+// Operand layouts (v_mfma_f32_16x16x32_f16; l = lane, g4 = l / 16):
+//   scores   A = 16 tokens (row l % 16) x 32 channels, B = 32 channels x 16
+//            query rows (column l % 16), C = lane holds tokens 4 g4 + 0..3 of
+//            query row l % 16;
+//   output   A = 16 channels x 32 tokens (V transposed), B = 32 tokens x 16
+//            query rows, C = lane holds channels 4 g4 + 0..3 of row l % 16.
+// The order of the contracted index is free as long as A and B agree. So a
+// lane's score results are its B operand of the second product as they are
+// (no exchange between lanes), and the nibbles of a dword are masked in
+// place: halves (n, n + 4) of a dword come out of one AND, as binary16
+// subnormals n * 2^-24 (K) or, with an OR and a packed add, as c - 8 (V); odd
+// nibbles come out 16 times too large, which the other operand makes good.
+// V's codes are stored token by token; ds_read_b64_tr_b4 transposes 16 x 16
+// nibbles among 16 lanes as it reads them.
+//
+// Work. The rows of a request and key/value head are its new tokens times the
+// query heads that share the head, alike to the kernels. attn_few.hpp takes up
+// to 32 of them (decode steps, checks of a few tokens) and gives the waves of a
+// workgroup different tokens; attn_rows.hpp takes more and gives them different
+// rows of the same tokens. Where there are few workgroups the tokens are cut
+// into `nsplit` chunks; partial results (reference, sum, output) are joined by
+// attn_join.hpp in a fixed order.
+#pragma once
+
+#include "kv_cache.hpp"
+
+namespace qg {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+struct AttnParams {
+    const void *q;
+    int64_t q_stride;
+    KvView kv;
+    const int32_t *table;
+    int64_t table_stride;
+    const int32_t *cu_q, *kv_len;
+    int batch;
+    int64_t total_q;
+    int32_t max_kv;
+    int group;            // query heads of one key/value head
+    int q_heads;
+    float scale_log2e;
+    int32_t window;       // 0: none
+    void *out;
+    int64_t out_stride;
+    float *lse;
+    float *part_out;      // [total_q * q_heads][nsplit][D]
+    float *part_stat;     // [total_q * q_heads][nsplit][2]: reference, sum
+    int nsplit;
+    int32_t chunk;        // tokens of a split (a multiple of the tile of a workgroup)
+};
+
+constexpr int kAttnThreads = 256;
+constexpr float kNoReference = -1e30f;   // below every score; finite, so that differences stay defined
+// A weight times a value scale stays below 2^(kHead + kSlack) in binary16;
+// the reference moves only when a score passes it by kSlack, so the
+// accumulators are rarely rescaled.
+constexpr float kHead = 7.0f, kSlack = 7.0f;
+
+// The rows of one tile of query rows: request b, rows row0.. of its rows
+// (row = token * group + head), and the tokens [lo, hi) that any of them sees.
+struct RowTile {
+    int b;
+    int32_t q0;           // first query row of the request in the batch
+    int32_t n_q, kv;      // its new tokens and its tokens
+    int64_t row0, rows;
+    int32_t first, last;  // tokens of its first and its last row (below 0: before the request)
+    int32_t lo, hi;
+    bool poison;          // longer than the call allows
+};
+
+__device__ __forceinline__ int32_t attn_cu(const AttnParams &p, int b)
+{
+    const int64_t v = p.cu_q[b];
+    return static_cast<int32_t>(v < 0 ? 0 : v > p.total_q ? p.total_q : v);
+}
+
+// Tile slots are dealt to requests without their exact tile counts:
+// request b starts at slot floor(cu_q[b] * group / R) + b, which leaves room
+// for ceil(rows / R) tiles; slots in between are empty.
+template <int R>
+__device__ __forceinline__ int64_t tile_start(const AttnParams &p, int b)
+{
+    return int64_t(attn_cu(p, b)) * p.group / R + b;
+}
+
+__device__ __forceinline__ void tile_tokens(const AttnParams &p, RowTile &t, int64_t row0, int R)
+{
+    t.kv = p.kv_len[t.b] < 0 ? 0 : p.kv_len[t.b];
+    t.poison = t.kv > p.max_kv;
+    if (t.poison) t.kv = 0;
+    t.row0 = row0;
+    t.rows = int64_t(t.n_q) * p.group;
+    const int64_t last = row0 + R < t.rows ? row0 + R : t.rows;
+    t.first = t.kv - t.n_q + static_cast<int32_t>(row0 / p.group);
+    t.last = t.kv - t.n_q + static_cast<int32_t>((last - 1) / p.group);
+    t.hi = t.last < 0 ? 0 : t.last + 1;
+    const int64_t lo = p.window > 0 ? int64_t(t.first) - p.window + 1 : 0;
+    t.lo = lo < 0 ? 0 : lo < t.hi ? static_cast<int32_t>(lo) : t.hi;
+}
+
+template <int R>
+__device__ __forceinline__ bool find_tile(const AttnParams &p, int64_t slot, RowTile &t)
+{
+    const int lane = threadIdx.x & 63;
+    int count = 0;
+    for (int base = 0; base < p.batch; base += 64) {
+        const int b = base + lane;
+        const uint64_t m = __ballot(b < p.batch && tile_start<R>(p, b) <= slot);
+        count += __popcll(m);
+        if (m != ~0ull) break;
+    }
+    if (count == 0) return false;
+    t.b = count - 1;
+    t.q0 = attn_cu(p, t.b);
+    t.n_q = attn_cu(p, t.b + 1) - t.q0;
+    const int64_t row0 = (slot - tile_start<R>(p, t.b)) * R;
+    if (t.n_q <= 0 || row0 >= int64_t(t.n_q) * p.group) return false;
+    tile_tokens(p, t, row0, R);
+    return true;
+}
+
+// Eight nibbles of a dword as binary16 subnormals: halves (0,4), (1,5)*16,
+// (2,6), (3,7)*16, each times 2^-24.
+__device__ __forceinline__ f16x8 nibbles_tiny(uint32_t w)
+{
+    const uint32_t v = w >> 8;
+    const u32x4 r = {w & 0x000f000fu, w & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u};
+    return __builtin_bit_cast(f16x8, r);
+}
+
+// Masks and the bits of 1024 in registers: an AND and an OR with two literals
+// would not go into one instruction.
+struct NibbleBits {
+    uint32_t even = 0x000f000fu, odd = 0x00f000f0u, thousand = 0x64006400u;
+    __device__ NibbleBits() { asm("" : "+s"(even), "+s"(odd), "+v"(thousand)); }
+};
+
+// Eight nibbles as c - 8: halves (0,4), (1,5)*16, (2,6), (3,7)*16. With the
+// bits of 1024 set, a half is 1024 + nibble (or + 16 nibble) exactly.
+__device__ __forceinline__ f16x8 nibbles_centred(uint32_t w, const NibbleBits &k)
+{
+    const uint32_t v = w >> 8;
+    const f16x2 even = {(_Float16)-1032.0f, (_Float16)-1032.0f}, odd = {(_Float16)-1152.0f, (_Float16)-1152.0f};
+    auto put = [&](uint32_t x, uint32_t mask, f16x2 off) {
+        return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, (x & mask) | k.thousand) + off);
+    };
+    const u32x4 r = {put(w, k.even, even), put(w, k.odd, odd), put(v, k.even, even), put(v, k.odd, odd)};
+    return __builtin_bit_cast(f16x8, r);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b)
+{
+    const f16x2 h = {static_cast<_Float16>(a), static_cast<_Float16>(b)};
+    uint32_t v = __builtin_bit_cast(uint32_t, h);
+    // A remainder is taken against these bits: without this the compiler
+    // rounds a product twice, fused to binary16 for the remainder and by way
+    // of float32 for the pair, and one of some 8000 pairs differs.
+    asm("" : "+v"(v));
+    return v;
+}
+
+// A dword of codes as an operand. With float32 queries the codes are centred;
+// the matrix cores take subnormals, but keep fewer bits of sums of their
+// products (scores 5 times, outputs 8 times as far from the exact ones), which
+// bfloat16's own rounding covers, at 5 instead of 9 instructions a dword.
+template <bool CENTRED>
+__device__ __forceinline__ f16x8 nibbles(uint32_t w, const NibbleBits &k)
+{
+    if constexpr (CENTRED) return nibbles_centred(w, k);
+    else return nibbles_tiny(w);
+}
+
+// Maximum (NaN ignored) over the four lanes that share l % 16.
+__device__ __forceinline__ float max_over_groups(float v)
+{
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+template <typename T>
+__device__ __forceinline__ void store_out4(T *dst, f32x4 v);
+template <>
+__device__ __forceinline__ void store_out4<float>(float *dst, f32x4 v) { *reinterpret_cast<f32x4 *>(dst) = v; }
+template <>
+__device__ __forceinline__ void store_out4<uint16_t>(uint16_t *dst, f32x4 v)
+{
+    u32x2 w = {f32_to_bf16_bits(v[0]) | (f32_to_bf16_bits(v[1]) << 16), f32_to_bf16_bits(v[2]) | (f32_to_bf16_bits(v[3]) << 16)};
+    *reinterpret_cast<u32x2 *>(dst) = w;
+}
+
+__device__ __forceinline__ float attn_inverse(const RowTile &t, float total)
+{
+    return t.poison ? __builtin_nanf("") : total == 0.0f ? 0.0f : 1.0f / total;
+}
+__device__ __forceinline__ float attn_lse(const RowTile &t, float ref, float total)
+{
+    return t.poison ? __builtin_nanf("")
+           : total == 0.0f ? -__builtin_inff() : (ref + __log2f(total)) * 0.693147180559945309f;
+}
+
+template <bool MASKED>
+struct MaskTag {
+    static constexpr bool value = MASKED;
+};
+
+// The query rows of a wave (QT tiles of 16, a row to the four lanes that share
+// lane % 16): their operands, and the running sums of their output.
+template <typename T, int D, int QT>
+struct QueryRows {
+    static constexpr bool kTwo = sizeof(T) == 4;           // float32: two pieces
+    static constexpr int NG = D / 64;
+    static constexpr float kUnit = kTwo ? 1.0f : 5.9604644775390625e-08f;       // of a code as the matrix cores see it
+    f16x8 qh[QT][NG][2], ql[kTwo ? QT : 1][NG][2];
+    float qsum[QT][NG], factor[QT];
+    int32_t pos[QT];                                       // the row's token, -1 for no row
+    f32x4 acc[QT][D / 16];
+    float ref[QT], total[QT], bias[QT][NG];
+
+    __device__ __forceinline__ void load(const AttnParams &p, const RowTile &t, int kv_head, int64_t first, int lane)
+    {
+        const int col = lane & 15, g4 = lane >> 4;
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) {
+            const int64_t row = first + qt * 16 + col;
+            const bool live = row < t.rows;
+            const int32_t tok = live ? static_cast<int32_t>(row / p.group) : 0;
+            const int head = kv_head * p.group + (live ? static_cast<int>(row - int64_t(tok) * p.group) : 0);
+            pos[qt] = live ? t.kv - t.n_q + tok : -1;
+            const T *src = static_cast<const T *>(p.q) + int64_t(t.q0 + tok) * p.q_stride + int64_t(head) * D;
+            float x[NG][2][8];
+            float top = 0.0f;
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int st = 0; st < 2; ++st) {
+                    load8(src + g * 64 + g4 * 16 + st * 8, x[g][st]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        x[g][st][i] = live ? x[g][st][i] : 0.0f;
+                        top = fmaxf(top, fabsf(x[g][st][i]));
+                    }
+                }
+            top = max_over_groups(top);
+            // power of two that brings the row's largest element into [2^13, 2^14)
+            int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xff);
+            e = e < 40 ? 40 : e > 240 ? 240 : e;
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 + 127 - e) << 23);
+            // scores come out as (q * up) . (code * kUnit)
+            factor[qt] = p.scale_log2e / kUnit * __uint_as_float(static_cast<uint32_t>(127 - 13 - 127 + e) << 23);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int st = 0; st < 2; ++st) {
+                    u32x4 h, l;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float a = x[g][st][r] * up, b = x[g][st][r + 4] * up;
+                        sum += a + b;
+                        const float sa = r & 1 ? a * 0.0625f : a, sb = r & 1 ? b * 0.0625f : b;
+                        const uint32_t pair = pack_f16(sa, sb);
+                        const f16x2 hh = __builtin_bit_cast(f16x2, pair);
+                        h[r] = pair;
+                        l[r] = pack_f16(sa - static_cast<float>(hh[0]), sb - static_cast<float>(hh[1]));
+                    }
+                    qh[qt][g][st] = __builtin_bit_cast(f16x8, h);
+                    if constexpr (kTwo) ql[qt][g][st] = __builtin_bit_cast(f16x8, l);
+                }
+                sum = pair_sum<5>(pair_sum<4>(sum));
+                qsum[qt][g] = sum * kUnit;
+            }
+            ref[qt] = kNoReference;
+            total[qt] = 0.0f;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) bias[qt][g] = 0.0f;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) acc[qt][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+    }
+
+    // Adds group g's share of the scores of 16 tokens (this lane: 4 of them,
+    // with scales sc and biases bi): k0, k1 their codes.
+    __device__ __forceinline__ void score(int qt, int g, f16x8 k0, f16x8 k1, f32x4 sc, f32x4 bi, f32x4 &x) const
+    {
+        f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
+        c = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qh[qt][g][0], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qh[qt][g][1], c, 0, 0, 0);
+        if constexpr (kTwo) {
+            c = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, ql[qt][g][0], c, 0, 0, 0);
+            c = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, ql[qt][g][1], c, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (g == 0) x[i] = sc[i] * c[i];
+            else x[i] = fmaf(sc[i], c[i], x[i]);
+            x[i] = fmaf(bi[i], qsum[qt][g], x[i]);
+        }
+    }
+
+    // Scores of NA blocks of 16 tokens into weights, the reference and the
+    // sums scaled where a score passes it. `base` is the first block's first
+    // token, vscale[g * pitch + token] the value scales (odd tokens: / 16),
+    // `top` the largest of them; visible: bit a * 4 + i.
+    template <bool MASKED, int NA>
+    __device__ __forceinline__ void weigh(const AttnParams &p, int qt, f32x4 (&x)[NA], uint32_t &visible, const float *vscale,
+                                          int pitch, float top, int32_t base, int g4)
+    {
+        float m = kNoReference, scale = top;
+        if constexpr (MASKED) {
+            visible = 0;
+            scale = 0.0f;
+            const int32_t last = pos[qt] - base;
+            const int32_t first = p.window > 0 ? last - p.window + 1 : -1;
+#pragma unroll
+            for (int a = 0; a < NA; ++a) {
+                f32x4 sc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const f32x4 v = *reinterpret_cast<const f32x4 *>(vscale + g * pitch + a * 16 + g4 * 4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[i] = fmaxf(sc[i], fabsf(v[i]) * (i & 1 ? 16.0f : 1.0f));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = a * 16 + g4 * 4 + i;
+                    const bool see = tok <= last && tok >= first;
+                    visible |= see ? 1u << (a * 4 + i) : 0u;
+                    m = see ? fmaxf(m, x[a][i] * factor[qt]) : m;
+                    scale = see ? fmaxf(scale, sc[i]) : scale;
+                }
+            }
+        } else {
+            float hi = x[0][0];
+#pragma unroll
+            for (int a = 0; a < NA; ++a)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) hi = fmaxf(hi, x[a][i]);
+            m = fmaxf(m, hi * factor[qt]);
+        }
+        // every value scale is below 2^es; the reference of a row is moved by
+        // what the row sees alone, so that nothing masked, and no other row,
+        // changes a bit of it
+        int es = static_cast<int>((__float_as_uint(scale) >> 23) & 0xff) - 126;
+        es = es < -60 ? -60 : es > 100 ? 100 : es;
+        const float want = m + (static_cast<float>(es) - kHead);
+        if (__any(want > ref[qt] + kSlack)) {
+            const float most = max_over_groups(want);      // the four lanes of a row move together
+            const float next = most > ref[qt] + kSlack ? most : ref[qt];
+            const float shrink = __builtin_amdgcn_exp2f(ref[qt] - next);
+            ref[qt] = next;
+            total[qt] *= shrink;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) bias[qt][g] *= shrink;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) acc[qt][d] *= shrink;
+        }
+#pragma unroll
+        for (int a = 0; a < NA; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float w = __builtin_amdgcn_exp2f(fmaf(x[a][i], factor[qt], -ref[qt]));
+                if constexpr (MASKED) w = visible >> (a * 4 + i) & 1u ? w : 0.0f;
+                x[a][i] = w;
+                total[qt] += w;
+            }
+    }
+
+    // Weights of 32 tokens (two blocks; value scales sc, biases bi of this
+    // lane's) as the B operand of group g's output; their biases added up.
+    template <bool MASKED>
+    __device__ __forceinline__ void pieces(int qt, int g, f32x4 w0, f32x4 w1, uint32_t visible, const f32x4 (&sc)[2],
+                                           const f32x4 (&bi)[2], f16x8 &ph, f16x8 &pl)
+    {
+        u32x4 hi, lo;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float s0 = sc[0][r], s1 = sc[1][r], b0 = bi[0][r], b1 = bi[1][r];
+            if constexpr (MASKED) {
+                // coefficients of tokens the row does not see may be anything
+                const bool see0 = visible >> r & 1u, see1 = visible >> (4 + r) & 1u;
+                s0 = see0 ? s0 : 0.0f, b0 = see0 ? b0 : 0.0f;
+                s1 = see1 ? s1 : 0.0f, b1 = see1 ? b1 : 0.0f;
+            }
+            bias[qt][g] = fmaf(w0[r], b0, bias[qt][g]);
+            bias[qt][g] = fmaf(w1[r], b1, bias[qt][g]);
+            const uint32_t pair = pack_f16(w0[r] * s0, w1[r] * s1);
+            hi[r] = pair;
+            if constexpr (kTwo) {
+                const f16x2 hh = __builtin_bit_cast(f16x2, pair);
+                lo[r] = pack_f16(fmaf(w0[r], s0, -static_cast<float>(hh[0])), fmaf(w1[r], s1, -static_cast<float>(hh[1])));
+            }
+        }
+        ph = __builtin_bit_cast(f16x8, hi);
+        if constexpr (kTwo) pl = __builtin_bit_cast(f16x8, lo);
+    }
+
+    // Channels 16 db.. of the output: v the codes of 32 tokens.
+    __device__ __forceinline__ void add(int qt, int db, f16x8 v, f16x8 ph, f16x8 pl)
+    {
+        acc[qt][db] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, ph, acc[qt][db], 0, 0, 0);
+        if constexpr (kTwo) acc[qt][db] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pl, acc[qt][db], 0, 0, 0);
+    }
+
+    // The lanes' sums joined, the biases added to the outputs.
+    __device__ __forceinline__ void close()
+    {
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) {
+            total[qt] = pair_sum<5>(pair_sum<4>(total[qt]));
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float b = pair_sum<5>(pair_sum<4>(bias[qt][g]));
+#pragma unroll
+                for (int db = 0; db < 4; ++db) {
+                    if constexpr (!kTwo) acc[qt][g * 4 + db] *= 1.0f / kUnit;
+                    acc[qt][g * 4 + db] += b;
+                }
+            }
+        }
+    }
+
+    // Results of a split, or of the whole call.
+    __device__ __forceinline__ void write(const AttnParams &p, const RowTile &t, int kv_head, int64_t first, int lane) const
+    {
+        const int col = lane & 15, g4 = lane >> 4;
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) {
+            const int64_t row = first + qt * 16 + col;
+            if (row >= t.rows) continue;
+            const int32_t tok = static_cast<int32_t>(row / p.group);
+            const int head = kv_head * p.group + static_cast<int>(row - int64_t(tok) * p.group);
+            const int64_t orow = int64_t(t.q0 + tok) * p.q_heads + head;
+            if (p.nsplit > 1) {
+                float *dst = p.part_out + (orow * p.nsplit + blockIdx.y) * D;
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) *reinterpret_cast<f32x4 *>(dst + d * 16 + g4 * 4) = acc[qt][d];
+                if (g4 == 0) {
+                    float *st = p.part_stat + (orow * p.nsplit + blockIdx.y) * 2;
+                    st[0] = ref[qt], st[1] = total[qt];
+                }
+            } else {
+                const float inv = attn_inverse(t, total[qt]);
+                T *dst = static_cast<T *>(p.out) + int64_t(t.q0 + tok) * p.out_stride + int64_t(head) * D;
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) store_out4(dst + d * 16 + g4 * 4, acc[qt][d] * inv);
+                if (p.lse && g4 == 0) p.lse[orow] = attn_lse(t, ref[qt], total[qt]);
+            }
+        }
+    }
+};
+
+// This split's tokens [begin, end) of a tile of rows; false: none, and not
+// the split that writes the results of rows without tokens.
+__device__ __forceinline__ bool split_tokens(const AttnParams &p, const RowTile &t, int tile, int32_t &begin, int32_t &end)
+{
+    const int64_t b = int64_t(t.lo / tile * tile) + int64_t(blockIdx.y) * p.chunk;
+    begin = b < t.hi ? static_cast<int32_t>(b) : t.hi;
+    end = t.hi - begin < p.chunk ? t.hi : begin + p.chunk;
+    return begin < end || blockIdx.y == 0;
+}
+
+// Whether every row of the tile sees all of `count` tokens from `base` on.
+__device__ __forceinline__ bool all_visible(const AttnParams &p, const RowTile &t, int32_t base, int count)
+{
+    return base + count - 1 <= t.first && (p.window <= 0 || base > t.last - p.window);
+}
+
+// Maximum of a non-negative value over each run of 16 lanes.
+__device__ __forceinline__ float max_over_16(float v)
+{
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false)));
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false)));
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xF, 0xF, false)));
+    return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, false)));
+}
+
+// Coefficients of a token's groups (scale low, bias high), `known`: its page
+// is in the cache, `inside`: it is one of the request's tokens.
+template <int NG>
+__device__ __forceinline__ void load_coefs(const uint8_t *src, bool known, bool inside, uint32_t (&c)[NG])
+{
+    if constexpr (NG == 1) {
+        c[0] = *reinterpret_cast<const uint32_t *>(src);
+    } else if constexpr (NG == 2) {
+        const u32x2 v = *reinterpret_cast<const u32x2 *>(src);
+        c[0] = v[0], c[1] = v[1];
+    } else {
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(src);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) c[g] = v[g];
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        if (!known) c[g] = 0x7fc07fc0u;      // a page outside the cache reads as NaN
+        if (!inside) c[g] = 0;               // places behind the last token hold anything
+    }
+}
+
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+
+// 16 x 16 nibbles transposed among 16 lanes: lane i addresses row i (8 bytes),
+// and gets nibble i of every row.
+__device__ __forceinline__ i32x2 read_transposed(const uint8_t *row)
+{
+    typedef __attribute__((address_space(3))) i32x2 *LdsPtr;
+    return __builtin_amdgcn_ds_read_tr4_b64_v2i32((LdsPtr)(__attribute__((address_space(3))) void *)(row));
+}
+
+// One wave's LDS operations complete in order; this keeps the compiler from
+// moving reads of what other lanes wrote ahead of the writes.
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+}  // namespace qg
