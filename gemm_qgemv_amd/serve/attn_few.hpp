@@ -36,7 +36,7 @@ struct TileLds {
     static constexpr int kTok = TOK;
     static constexpr int kRow = D / 2;                     // code bytes of a token
     uint8_t codes[2 * kTok * kRow];                        // K, V
-    // scale (V, odd tokens: / 16) and bias (float32 queries: + 8 scale) of K, V
+    // scale (V, odd tokens: / 16) and bias (float32 queries: + centre * scale) of K, V
     float co[2][D / 64][2][kTok];
     float top[4];                                          // largest |value scale| of a staging wave
 };
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_few_kernel(AttnParams p)
     auto put_tile = [&](Tile &s) {
         float top = 0.0f;
         const bool is_v = (lane >> 4) & 1;
-        const float odd = is_v && (lane & 1) ? 0.0625f : 1.0f;
+        const float odd = is_v && (lane & 1) ? 0.0625f : 1.0f, centre = is_v && (lane & 1) ? kOddCentre : 8.0f;
 #pragma unroll
         for (int j = 0; j < NBW; ++j) {
             const int blk = rw + j * RW;
@@ -146,7 +146,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_few_kernel(AttnParams p)
                 top = fmaxf(top, fabsf(sc));
                 if (lane < 32) {
                     s.co[is_v][g][0][blk * 16 + (lane & 15)] = sc * odd;
-                    s.co[is_v][g][1][blk * 16 + (lane & 15)] = kTwo ? fmaf(8.0f, sc, bi) : bi;
+                    s.co[is_v][g][1][blk * 16 + (lane & 15)] = kTwo ? fmaf(centre, sc, bi) : bi;
                 }
             }
         }
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_few_kernel(AttnParams p)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t codes = h ? static_cast<uint32_t>(w[1]) : static_cast<uint32_t>(w[0]);
-                    rows.add(0, kBlocks == 1 ? g * 4 + n : g * 4 + n * 2 + h, nibbles<kTwo>(codes, bits), ph[kBlocks == 1 ? h : 0],
+                    rows.add(0, kBlocks == 1 ? g * 4 + n : g * 4 + n * 2 + h, nibbles<kTwo, kOddCentre>(codes, bits), ph[kBlocks == 1 ? h : 0],
                              pl[kBlocks == 1 ? h : 0]);
                 }
             }

@@ -125,14 +125,14 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_rows_kernel(AttnParams p
         if (NB == 4 || wave < NB) {
             float top = 0.0f;
             const bool is_v = (lane >> 4) & 1;
-            const float odd = is_v && (lane & 1) ? 0.0625f : 1.0f;
+            const float odd = is_v && (lane & 1) ? 0.0625f : 1.0f, centre = is_v && (lane & 1) ? kOddCentre : 8.0f;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 const float sc = __uint_as_float(coef[g] << 16), bi = __uint_as_float(coef[g] & 0xffff0000u);
                 top = fmaxf(top, fabsf(sc));
                 if (lane < 32) {
                     s.co[is_v][g][0][k_block * 16 + (lane & 15)] = sc * odd;
-                    s.co[is_v][g][1][k_block * 16 + (lane & 15)] = kTwo ? fmaf(8.0f, sc, bi) : bi;
+                    s.co[is_v][g][1][k_block * 16 + (lane & 15)] = kTwo ? fmaf(centre, sc, bi) : bi;
                 }
             }
             top = max_over_16(top);
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_rows_kernel(AttnParams p
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 s.v[v_half][v_part * (VB / 8) + n * 2 + h][lane] =
-                    __builtin_bit_cast(u32x4, nibbles<kTwo>(h ? static_cast<uint32_t>(w[1]) : static_cast<uint32_t>(w[0]), bits));
+                    __builtin_bit_cast(u32x4, nibbles<kTwo, kOddCentre>(h ? static_cast<uint32_t>(w[1]) : static_cast<uint32_t>(w[0]), bits));
         }
         wave_fence();
     };
