@@ -35,10 +35,13 @@ AttnPlan plan_attn(const qg_kv_cache &c, int batch, int64_t total_q, int64_t max
     a.slots = total_q * group / a.rows + batch;
     a.tile = few_or_rows_tile(c.head_dim, a.rows);
     a.step = a.tile * (a.rows == 16 ? 4 : a.rows == 32 ? 2 : 1);
-    // two workgroups on every compute unit
+    // two workgroups on every compute unit; four where decoding requests may
+    // differ in length (64 requests of 1024 to 8192 tokens: 117 us at two, 91
+    // at four, 94 at eight; one request of 131071: 50 at two, 53 at four)
     const int64_t tiles = std::max<int64_t>(1, total_q * group / a.rows);
     const int64_t have = std::max(tiles, std::min<int64_t>(batch, total_q)) * c.kv_heads;
-    const int64_t want = std::max<int64_t>(1, (2 * kComputeUnits + have / 2) / have);
+    const int64_t aim = (a.rows == 16 && batch > 1 ? 4 : 2) * kComputeUnits;
+    const int64_t want = std::max<int64_t>(1, (aim + have / 2) / have);
     a.nsplit = static_cast<int>(std::clamp<int64_t>(want, 1, std::min<int64_t>(ceil_div(max_kv, a.step), qg::kMaxSplits)));
     // a tile's first token is rounded down to a tile: one more
     a.chunk = static_cast<int32_t>(round_up(ceil_div(max_kv + a.tile, a.nsplit), a.step));

@@ -84,7 +84,7 @@ int qkv_plan(const int32_t *len_old, const int32_t *keep, const int32_t *n_new, 
                                    hipFuncAttributeMaxDynamicSharedMemorySize, (3 * QG_MAX_PLAN_BATCH + 1) * 4) == hipSuccess;
     }();
     (void)allowed;
-    hipLaunchKernelGGL(qg::kv_plan_kernel, dim3(grid), dim3(qg::kPlanThreads), lds, stream, p);
+    hipLaunchKernelGGL(qg::kv_plan_kernel, dim3(grid, 3), dim3(qg::kPlanThreads), lds, stream, p);
     return launch_status();
 }
 

@@ -97,7 +97,7 @@ int qlogprobs(const float *logits, int64_t ld, int64_t rows, int64_t vocab, cons
     }
     hipLaunchKernelGGL(qg::logprob_kernel, dim3(static_cast<unsigned>(rows * a.nslice)), dim3(qg::kLpThreads), 0, stream, p);
     if (a.nslice > 1)
-        hipLaunchKernelGGL(qg::logprob_join_kernel, dim3(static_cast<unsigned>(rows)), dim3(qg::kLpThreads), 0, stream, p);
+        hipLaunchKernelGGL(qg::logprob_join_kernel, dim3(static_cast<unsigned>(rows)), dim3(qg::kLpJoinThreads), 0, stream, p);
     return launch_status();
 }
 

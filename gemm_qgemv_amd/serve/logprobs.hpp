@@ -11,9 +11,10 @@
 // The order of the alternatives (larger logit first, ties by lower index) is
 // that of the 64-bit keys argmax_key(x, index). A wave keeps its best 64 keys
 // sorted over its lanes; a block of 1024 logits is looked at for them only if
-// its maximum passes the last one wanted, which gets rare soon (a block is
-// one of n equal blocks so far: about top / n). The block's candidates, one a
-// lane, are sorted and merged into the list by bitonic networks over lanes.
+// its maximum passes the last one wanted, which gets rare soon (for the n-th
+// block about top / n). The block's candidates, one a lane in rounds, are
+// sorted and merged into the list by bitonic networks over lanes (DPP and
+// permlane swaps: no LDS round trips).
 //
 // A row is cut into slices over workgroups, each slice into runs of blocks
 // over 4 waves; the parts are joined over LDS and, with more than one slice,
@@ -63,39 +64,69 @@ __device__ __forceinline__ Moments lp_join(Moments a, Moments b)
     return {m, fmaf(fa, a.z, fb * b.z), fmaf(fa, fmaf(a.z, da, a.t), fb * fmaf(b.z, db, b.t))};
 }
 
-__device__ __forceinline__ uint64_t key_max(uint64_t a, uint64_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint64_t key_min(uint64_t a, uint64_t b) { return a < b ? a : b; }
-
-// Keys of a bitonic sequence over the 64 lanes into descending order.
-__device__ __forceinline__ uint64_t bitonic_merge(uint64_t k, int lane)
+// Value of lane ^ D by DPP (D = 1, 2, 4, 8: no LDS round trip).
+template <int D>
+__device__ __forceinline__ uint32_t near_u32(uint32_t v)
 {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-        const uint64_t o = shfl_xor_u64(k, d);
-        k = lane & d ? key_min(k, o) : key_max(k, o);
+    static_assert(D == 1 || D == 2 || D == 4 || D == 8, "within 16 lanes");
+    if constexpr (D == 4) {
+        // mirrored within 8 lanes (lane ^ 7), then within 4 (lane ^ 3)
+        v = __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, false);
+        return __builtin_amdgcn_update_dpp(0, v, 0x1B, 0xF, 0xF, false);
+    } else {
+        constexpr int ctrl = D == 1 ? 0xB1 : D == 2 ? 0x4E : 0x128;
+        return __builtin_amdgcn_update_dpp(0, v, ctrl, 0xF, 0xF, false);
     }
-    return k;
+}
+
+// The larger (or the smaller) of a lane's key and that of lane ^ D.
+template <int D>
+__device__ __forceinline__ uint64_t exchange(uint64_t k, bool keep_max)
+{
+    const uint32_t lo = static_cast<uint32_t>(k), hi = static_cast<uint32_t>(k >> 32);
+    uint64_t a, b;
+    if constexpr (D <= 8) {
+        a = k;
+        b = (static_cast<uint64_t>(near_u32<D>(hi)) << 32) | near_u32<D>(lo);
+    } else {
+        // both partners get the same pair: the swaps return it in either lane
+        const auto rl = D == 16 ? __builtin_amdgcn_permlane16_swap(lo, lo, false, false) : __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
+        const auto rh = D == 16 ? __builtin_amdgcn_permlane16_swap(hi, hi, false, false) : __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+        a = (static_cast<uint64_t>(rh[0]) << 32) | rl[0];
+        b = (static_cast<uint64_t>(rh[1]) << 32) | rl[1];
+    }
+    return (a > b) == keep_max ? a : b;
+}
+
+// One run of exchange steps W / 2, .., 1 of a bitonic network over the 64
+// lanes; lanes of runs of W in turn sort up and down (W = 64: all down).
+template <int W, int D>
+__device__ __forceinline__ uint64_t bitonic_steps(uint64_t k, int lane)
+{
+    if constexpr (D >= 1) {
+        k = exchange<D>(k, ((lane & D) == 0) == ((lane & W) == 0));
+        return bitonic_steps<W, D / 2>(k, lane);
+    } else {
+        return k;
+    }
 }
 
 // Any 64 keys into descending order over the lanes.
 __device__ __forceinline__ uint64_t bitonic_sort(uint64_t k, int lane)
 {
-#pragma unroll
-    for (int w = 2; w <= 64; w <<= 1)
-#pragma unroll
-        for (int d = w >> 1; d >= 1; d >>= 1) {
-            const uint64_t o = shfl_xor_u64(k, d);
-            const bool keep_max = ((lane & d) == 0) == ((lane & w) == 0);
-            k = keep_max ? key_max(k, o) : key_min(k, o);
-        }
-    return k;
+    k = bitonic_steps<2, 1>(k, lane);
+    k = bitonic_steps<4, 2>(k, lane);
+    k = bitonic_steps<8, 4>(k, lane);
+    k = bitonic_steps<16, 8>(k, lane);
+    k = bitonic_steps<32, 16>(k, lane);
+    return bitonic_steps<64, 32>(k, lane);
 }
 
 // The 64 largest of two descending lists, descending.
 __device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b, int lane)
 {
     const uint64_t r = shfl_xor_u64(b, 63);          // reversed
-    return bitonic_merge(key_max(a, r), lane);
+    return bitonic_steps<64, 32>(a > r ? a : r, lane);
 }
 
 __device__ __forceinline__ uint64_t lane_u64(uint64_t v, int src)
@@ -117,30 +148,34 @@ struct RowResult {
     uint64_t list;               // lane i: the i-th best key
 };
 
-// The results of the workgroup's waves joined, in every wave.
+// The results of the workgroup's WAVES waves joined (the list: in wave 0).
+template <int WAVES>
 __device__ __forceinline__ RowResult lp_join_waves(RowResult r, bool want_top)
 {
-    __shared__ f32x4 stat[kLpWaves];
-    __shared__ uint64_t lists[kLpWaves][64];
+    __shared__ f32x4 stat[WAVES];
+    __shared__ uint64_t lists[WAVES][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    __syncthreads();
     if (lane == 0) stat[wave] = f32x4{r.mo.m, r.mo.z, r.mo.t, __int_as_float(r.before)};
-    if (want_top) lists[wave][lane] = r.list;
-    __syncthreads();
+    if (want_top) {
+        // halves of the waves hand their lists to the other halves
+#pragma unroll
+        for (int n = WAVES / 2; n >= 1; n >>= 1) {
+            if (wave >= n && wave < 2 * n) lists[wave][lane] = r.list;
+            __syncthreads();
+            if (wave < n) r.list = merge_lists(r.list, lists[wave + n][lane], lane);
+        }
+    } else {
+        __syncthreads();
+    }
     RowResult o;
     o.mo = {kLowest, 0.0f, 0.0f};
     o.before = 0;
-    o.list = 0;
-#pragma unroll
-    for (int w = 0; w < kLpWaves; ++w) {
+    o.list = r.list;
+#pragma unroll 4
+    for (int w = 0; w < WAVES; ++w) {
         const f32x4 s = stat[w];
         o.mo = lp_join(o.mo, {s[0], s[1], s[2]});
         o.before += __float_as_int(s[3]);
-    }
-    if (want_top && wave == 0) {
-        o.list = lists[0][lane];
-#pragma unroll
-        for (int w = 1; w < kLpWaves; ++w) o.list = merge_lists(o.list, lists[w][lane], lane);
     }
     return o;
 }
@@ -260,21 +295,31 @@ __global__ __launch_bounds__(kLpThreads) void logprob_kernel(LogprobParams p)
         }
 
         if (top > 0 && (last_key == 0 || __any(bm > last))) {
-            uint64_t used = ~0ull;                   // this lane's keys from here on are below
+            // the block's values in their order (0: not of the row, or taken)
+            uint32_t order[4 * kLpQuads];
+#pragma unroll
+            for (int j = 0; j < kLpQuads; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int32_t i = at(j) + e;
+                    order[j * 4 + e] = inner || (i >= 0 && i < p.vocab) ? float_order_bits(v[j][e]) : 0;
+                }
+            // a lane's best value that is left, in rounds until none passes the list's last
             for (;;) {
-                uint64_t best = 0;
+                uint32_t best = order[0];
+                int slot = 0;
 #pragma unroll
-                for (int j = 0; j < kLpQuads; ++j)
+                for (int n = 1; n < 4 * kLpQuads; ++n) {
+                    slot = order[n] > best ? n : slot;           // the first of equal ones
+                    best = order[n] > best ? order[n] : best;
+                }
+                const uint32_t index = static_cast<uint32_t>(at(slot >> 2) + (slot & 3));
+                const uint64_t key = best ? (static_cast<uint64_t>(best) << 32) | (0xFFFFFFFFu - index) : 0;
+                const bool passes = key > last_key;
+                if (!__any(passes)) break;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int32_t i = at(j) + e;
-                        const bool in = inner || (i >= 0 && i < p.vocab);
-                        const uint64_t k = in ? argmax_key(v[j][e], static_cast<uint32_t>(i)) : 0;
-                        best = k < used && k > last_key ? key_max(best, k) : best;
-                    }
-                if (!__any(best != 0)) break;
-                used = best;
-                r.list = merge_lists(r.list, bitonic_sort(best, lane), lane);
+                for (int n = 0; n < 4 * kLpQuads; ++n) order[n] = n == slot ? 0 : order[n];
+                r.list = merge_lists(r.list, bitonic_sort(passes ? key : 0, lane), lane);
                 last_key = lane_u64(r.list, top - 1);
                 last = key_value(last_key);
             }
@@ -288,7 +333,7 @@ __global__ __launch_bounds__(kLpThreads) void logprob_kernel(LogprobParams p)
         // both partners add in the same order
         r.mo = lane & d ? lp_join(o, r.mo) : lp_join(r.mo, o);
     }
-    r = lp_join_waves(r, top > 0);
+    r = lp_join_waves<kLpWaves>(r, top > 0);
     if (p.nslice == 1) {
         lp_finish(p, row, r);
     } else if (wave == 0) {
@@ -298,22 +343,26 @@ __global__ __launch_bounds__(kLpThreads) void logprob_kernel(LogprobParams p)
 }
 
 // Joins the slices of a row.
-__global__ __launch_bounds__(kLpThreads) void logprob_join_kernel(LogprobParams p)
+constexpr int kLpJoinThreads = 1024;
+
+__global__ __launch_bounds__(kLpJoinThreads) void logprob_join_kernel(LogprobParams p)
 {
+    constexpr int kWaves = kLpJoinThreads / 64;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t row = blockIdx.x;
     RowResult r;
     r.mo = {kLowest, 0.0f, 0.0f};
     r.before = 0;
     r.list = 0;
-    for (int s = wave; s < p.nslice; s += kLpWaves) {
+    for (int s = wave; s < p.nslice; s += kWaves) {
         const int64_t at = row * p.nslice + s;
         const f32x4 v = p.part[at];
+        const uint64_t list = lane < p.top ? p.part_keys[at * p.top + lane] : 0;
         r.mo = lp_join(r.mo, {v[0], v[1], v[2]});
         r.before += __float_as_int(v[3]);
-        if (p.top > 0) r.list = merge_lists(r.list, lane < p.top ? p.part_keys[at * p.top + lane] : 0, lane);
+        if (p.top > 0) r.list = merge_lists(r.list, list, lane);
     }
-    r = lp_join_waves(r, p.top > 0);
+    r = lp_join_waves<kWaves>(r, p.top > 0);
     lp_finish(p, row, r);
 }
 
