@@ -55,53 +55,81 @@ __device__ __forceinline__ float reduce8(float v)
     return step(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, false)));
 }
 
-template <typename T>
-__global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendParams p)
+// A group of 64 values (8 lanes of 8) as bf16 bits of scale and bias (low and
+// high half of `coef`) and this lane's 8 codes.
+__device__ __forceinline__ void quantize_group(const float (&x)[8], int lane, uint32_t &codes, uint32_t &coef)
 {
-    const int part = blockIdx.y;
-    int64_t t;
-    int c;
-    if (!append_place(p.map, p.n, t, c)) return;     // whole runs of 8 lanes leave together
-    const int64_t slot = p.slots[t];
-    const int64_t page = slot >> p.kv.page_shift;
-    if (slot < 0 || page >= p.kv.num_pages) return;
-    const int head = c >> p.kv.dim_shift, d = c & (p.kv.dim - 1);
-
-    float x[8];
-    load8(static_cast<const T *>(p.src[part]) + t * p.stride[part] + c, x);
     float lo = x[0], hi = x[0];
-    bool finite = true;
+    uint32_t largest = 0;                         // as bits: not finite from 0x7f800000 on
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         lo = fminf(lo, x[i]);
         hi = fmaxf(hi, x[i]);
-        finite = finite && fabsf(x[i]) <= 3.402823466e38f;
+        largest = max(largest, __float_as_uint(x[i]) & 0x7fffffffu);
     }
     lo = reduce8<false>(lo);
     hi = reduce8<true>(hi);
-    const int lane = threadIdx.x & 63;
-    const uint64_t ok = __ballot(finite);
-    uint32_t sb = f32_to_bf16_bits((hi - lo) / 15.0f);
-    uint32_t bb = f32_to_bf16_bits(lo);
+    const uint64_t ok = __ballot(largest < 0x7f800000u);
+    const uint32_t both = f32_to_bf16_pair((hi - lo) / 15.0f, lo);
+    uint32_t sb = both & 0xffffu, bb = both >> 16;
     const bool good = ((ok >> (lane & 56)) & 0xff) == 0xff && (sb & 0x7f80u) != 0x7f80u && (bb & 0x7f80u) != 0x7f80u;
     if ((sb & 0x7f80u) == 0) sb = 0;              // below the least normal: the group is its minimum
     if (!good) sb = bb = 0x7fc0u;
-    const float s = bf16_bits_to_f32(sb), b = bf16_bits_to_f32(bb);
-    uint32_t codes = 0;
+    coef = sb | (bb << 16);
+    codes = 0;
     if (good && sb != 0) {
+        const float s = bf16_bits_to_f32(sb), b = bf16_bits_to_f32(bb), inv = 1.0f / s;
         float q[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = fminf(fmaxf(__builtin_rintf((x[i] - b) / s), 0.0f), 15.0f);
+        for (int i = 0; i < 8; ++i) {
+            // the correctly rounded quotient: with inv the correctly rounded
+            // reciprocal, one exact remainder corrects d * inv (Markstein,
+            // "Computation of elementary functions on the IBM RISC System/6000
+            // processor", 1990); 3 operations for a division's 10
+            const float d = x[i] - b, q0 = d * inv;
+            q[i] = fmaf(fmaf(-q0, s, d), inv, q0);
+        }
+        // scales whose reciprocal or remainders leave the normal range
+        if (s <= 0x1p-100f || s >= 0x1p100f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[i] = (x[i] - b) / s;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = __builtin_amdgcn_fmed3f(__builtin_rintf(q[i]), 0.0f, 15.0f);
         // four codes side by side are exact in a float32
         const float q0 = fmaf(4096.0f, q[3], fmaf(256.0f, q[2], fmaf(16.0f, q[1], q[0])));
         const float q1 = fmaf(4096.0f, q[7], fmaf(256.0f, q[6], fmaf(16.0f, q[5], q[4])));
         codes = static_cast<uint32_t>(q0) | (static_cast<uint32_t>(q1) << 16);
     }
+}
+
+// A lane takes 8 channels of K and of V: both loads, and the slot's, are in
+// flight together (what bounds it is how long they take).
+template <typename T>
+__global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendParams p)
+{
+    int64_t t;
+    int c;
+    if (!append_place(p.map, p.n, t, c)) return;     // whole runs of 8 lanes leave together
+    const int64_t slot = p.slots[t];
+    float x[2][8];
+    load8(static_cast<const T *>(p.src[0]) + t * p.stride[0] + c, x[0]);
+    load8(static_cast<const T *>(p.src[1]) + t * p.stride[1] + c, x[1]);
+    const int lane = threadIdx.x & 63;
+    uint32_t codes[2], coef[2];
+#pragma unroll
+    for (int part = 0; part < 2; ++part) quantize_group(x[part], lane, codes[part], coef[part]);
+    const int64_t page = slot >> p.kv.page_shift;
+    if (slot < 0 || page >= p.kv.num_pages) return;
+    const int head = c >> p.kv.dim_shift, d = c & (p.kv.dim - 1);
     uint8_t *block = p.kv.data + page * p.kv.page_bytes + int64_t(head) * p.kv.block_bytes;
     const int at = static_cast<int>(slot) & ((1 << p.kv.page_shift) - 1);
-    *reinterpret_cast<uint32_t *>(block + kv_part(p.kv, part) + at * (p.kv.dim / 2) + d / 2) = codes;
-    if ((lane & 7) == 0)
-        *reinterpret_cast<uint32_t *>(block + kv_coefs(p.kv, part) + at * kv_coef_bytes(p.kv.dim) + d / 16) = sb | (bb << 16);
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+        *reinterpret_cast<uint32_t *>(block + kv_part(p.kv, part) + at * (p.kv.dim / 2) + d / 2) = codes[part];
+        if ((lane & 7) == 0)
+            *reinterpret_cast<uint32_t *>(block + kv_coefs(p.kv, part) + at * kv_coef_bytes(p.kv.dim) + d / 16) = coef[part];
+    }
 }
 
 struct ReadParams {

@@ -212,7 +212,7 @@ __device__ __forceinline__ void store_out4<float>(float *dst, f32x4 v) { *reinte
 template <>
 __device__ __forceinline__ void store_out4<uint16_t>(uint16_t *dst, f32x4 v)
 {
-    u32x2 w = {f32_to_bf16_bits(v[0]) | (f32_to_bf16_bits(v[1]) << 16), f32_to_bf16_bits(v[2]) | (f32_to_bf16_bits(v[3]) << 16)};
+    const u32x2 w = {f32_to_bf16_pair(v[0], v[1]), f32_to_bf16_pair(v[2], v[3])};
     *reinterpret_cast<u32x2 *>(dst) = w;
 }
 

@@ -23,13 +23,14 @@ Range rows_range(int dtype, const void *p, int64_t stride, int64_t width, int64_
     return range_of(p, ((n - 1) * stride + width) * (dtype == QG_F32 ? 4 : 2));
 }
 
-qg::AppendMap append_map(const qg_kv_cache &c, int64_t n, dim3 &grid)
+// `parts`: K and V in workgroups of their own (2) or together (1).
+qg::AppendMap append_map(const qg_kv_cache &c, int64_t n, unsigned parts, dim3 &grid)
 {
     qg::AppendMap m;
     m.per_row = c.kv_heads * c.head_dim / 8;
     m.rows = std::max(1, qg::kAppendThreads / m.per_row);
     m.inv = 1.0f / static_cast<float>(m.per_row);
-    grid = dim3(static_cast<unsigned>(ceil_div(n, m.rows)), 2,
+    grid = dim3(static_cast<unsigned>(ceil_div(n, m.rows)), parts,
                 static_cast<unsigned>(ceil_div(m.per_row, qg::kAppendThreads)));
     return m;
 }
@@ -76,8 +77,10 @@ int qkv_plan(const int32_t *len_old, const int32_t *keep, const int32_t *n_new, 
     (void)hipGetLastError();
     qg::PlanParams p{len_old, keep, n_new, batch, __builtin_ctz(static_cast<unsigned>(page_size)), block_table,
                      table_stride, ring, ring_size, state_in, state_out, kv_len, cu_q, slots, pos, total, denied};
-    // eight tokens a thread: every workgroup repeats the running sums
-    const auto grid = static_cast<unsigned>(std::clamp<int64_t>(ceil_div(total, qg::kPlanThreads * 8), 1, 256));
+    // two tokens a thread (each takes a chain of LDS reads to find its request;
+    // every workgroup repeats the running sums; 65536 tokens of 512 requests: 13.3
+    // us at eight, 6.7 at two)
+    const auto grid = static_cast<unsigned>(std::clamp<int64_t>(ceil_div(total, qg::kPlanThreads * 2), 1, 256));
     const size_t lds = (3 * static_cast<size_t>(batch) + 1) * 4;
     static const bool allowed = [] {
         return hipFuncSetAttribute(reinterpret_cast<const void *>(qg::kv_plan_kernel),
@@ -109,7 +112,7 @@ int qkv_append(int dtype, const void *k, int64_t k_stride, const void *v, int64_
 
     (void)hipGetLastError();
     dim3 grid;
-    const qg::AppendMap map = append_map(*cache, n, grid);
+    const qg::AppendMap map = append_map(*cache, n, 1, grid);
     qg::AppendParams p{{k, v}, {k_stride, v_stride}, slots, n, map, kv_view(*cache)};
     if (dtype == QG_F32)
         hipLaunchKernelGGL(qg::kv_append_kernel<float>, grid, dim3(qg::kAppendThreads), 0, stream, p);
@@ -141,7 +144,7 @@ int qkv_read(int dtype, const qg_kv_cache *cache, const int32_t *slots, int64_t 
 
     (void)hipGetLastError();
     dim3 grid;
-    const qg::AppendMap map = append_map(*cache, n, grid);
+    const qg::AppendMap map = append_map(*cache, n, 2, grid);
     qg::ReadParams p{{k, v}, {k_stride, v_stride}, slots, n, map, kv_view(*cache)};
     if (dtype == QG_F32)
         hipLaunchKernelGGL(qg::kv_read_kernel<float>, grid, dim3(qg::kAppendThreads), 0, stream, p);

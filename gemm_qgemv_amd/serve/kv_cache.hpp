@@ -35,12 +35,18 @@ __device__ __forceinline__ int kv_coefs(const KvView &c, int part)
     return kv_part(c, part) + ((c.dim / 2) << c.page_shift);
 }
 
-// float32 -> bf16 bits, nearest even (NaN stays NaN: its payload's top bit is set).
+// float32 -> bf16 bits, nearest even (gfx950 converts; NaN stays NaN).
 __device__ __forceinline__ uint32_t f32_to_bf16_bits(float v)
 {
-    const uint32_t u = __float_as_uint(v);
-    if ((u & 0x7fffffffu) > 0x7f800000u) return (u >> 16) | 0x40u;
-    return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+
+// Two of them, the first in the low half.
+__device__ __forceinline__ uint32_t f32_to_bf16_pair(float a, float b)
+{
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 v = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+    return __builtin_bit_cast(uint32_t, v);
 }
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -81,7 +87,7 @@ __device__ __forceinline__ void store8<uint16_t>(uint16_t *dst, const float (&x)
 {
     u32x4 v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = f32_to_bf16_bits(x[2 * i]) | (f32_to_bf16_bits(x[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) v[i] = f32_to_bf16_pair(x[2 * i], x[2 * i + 1]);
     *reinterpret_cast<u32x4 *>(dst) = v;
 }
 
