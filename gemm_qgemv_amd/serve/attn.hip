@@ -19,6 +19,19 @@ struct AttnPlan {
     int tile, step;        // tokens of a tile, and of a workgroup's round of tiles
     int nsplit;
     int32_t chunk;
+
+    // at most `most` splits of `tokens` tokens, of whole rounds. A few rounds
+    // stay in one split: the join would take longer (one row of 4 heads at 500
+    // tokens, 2 rounds: 10 us, 14 split; 16-row tiles at 3 rounds: 13.5 and 11.9;
+    // 40 rows at 130 tokens, 3 rounds: 16 us, 20 split, at 5 rounds 22 and 19)
+    void split(int64_t tokens, int64_t most)
+    {
+        const int64_t rounds = (tokens + step - 1) / step;
+        most = std::max<int64_t>(most, 1);
+        most = rounds <= (rows <= 32 ? 2 : 3) ? 1 : std::min(most, rounds);
+        chunk = static_cast<int32_t>((rounds + most - 1) / most * step);
+        nsplit = static_cast<int>((tokens + chunk - 1) / chunk);
+    }
 };
 
 constexpr int few_or_rows_tile(int dim, int rows)
@@ -37,26 +50,33 @@ AttnPlan plan_attn(const qg_kv_cache &c, int batch, int64_t total_q, int64_t max
     a.step = a.tile * (a.rows == 16 ? 4 : a.rows == 32 ? 2 : 1);
     // two workgroups on every compute unit; four where decoding requests may
     // differ in length (64 requests of 1024 to 8192 tokens: 117 us at two, 91
-    // at four, 94 at eight; one request of 131071: 50 at two, 53 at four)
+    // at four, 94 at eight; one request of 131071: 47 at two, 53 at four)
     const int64_t tiles = std::max<int64_t>(1, total_q * group / a.rows);
     const int64_t have = std::max(tiles, std::min<int64_t>(batch, total_q)) * c.kv_heads;
     const int64_t aim = (a.rows == 16 && batch > 1 ? 4 : 2) * kComputeUnits;
     const int64_t want = std::max<int64_t>(1, (aim + have / 2) / have);
-    a.nsplit = static_cast<int>(std::clamp<int64_t>(want, 1, std::min<int64_t>(ceil_div(max_kv, a.step), qg::kMaxSplits)));
-    // a tile's first token is rounded down to a tile: one more
-    a.chunk = static_cast<int32_t>(round_up(ceil_div(max_kv + a.tile, a.nsplit), a.step));
-    a.nsplit = static_cast<int>(ceil_div(max_kv + a.tile, a.chunk));
+    // n splits take a workgroup rounds / n rounds, of 2 us or so, and n partial
+    // results of every row written and read, at some terabytes a second: the
+    // least sum is at a root (1280 rows of 128 float32 channels, 4000 tokens:
+    // 31 us in 32 splits, 39 in 63; 512 rows of 256, 12000 tokens: 30 us in 63
+    // splits, 39 in 188; decoding stays far below)
+    const double rounds = static_cast<double>(ceil_div(max_kv, a.step));
+    const double best = std::sqrt(rounds * 2e6 / (static_cast<double>(total_q) * q_heads * c.head_dim));
+    const int64_t most_splits = std::min<int64_t>({want, std::llround(best), qg::kMaxSplits});
+    // few splits of requests that may differ in length, half a round longer each:
+    // the last ones, which start last, are then short and even out the end (64
+    // requests as above: 91 us, 98 with all alike; to 14000 tokens, 16 requests:
+    // 43 and 50)
+    const bool even_out = a.rows <= 32 && batch > 1 && most_splits > 1 && most_splits <= 8;
+    a.split(max_kv + (even_out ? most_splits * a.step / 2 : 0), most_splits);
     return a;
 }
 
-// With a window a tile of rows sees at most window + rows tokens: as many
-// splits, of fewer tokens.
+// With a window a tile of rows sees at most window + rows tokens, from a first
+// one that is rounded down to a tile: no more splits, of fewer tokens.
 void narrow_plan(AttnPlan &a, int64_t max_kv, int64_t window)
 {
-    if (window >= max_kv) return;
-    const int64_t range = std::min<int64_t>(max_kv, window + a.rows) + a.tile;
-    a.chunk = static_cast<int32_t>(round_up(ceil_div(range, a.nsplit), a.step));
-    a.nsplit = static_cast<int>(ceil_div(range, a.chunk));
+    if (window < max_kv) a.split(std::min<int64_t>(max_kv, window + a.rows) + a.tile, a.nsplit);
 }
 
 size_t attn_workspace(const AttnPlan &a, const qg_kv_cache &c, int64_t total_q, int q_heads)
@@ -95,7 +115,10 @@ void launch_attn(const AttnPlan &a, const qg::AttnParams &p, hipStream_t s)
     if (a.nsplit == 1) return;
     constexpr int TOK = few_or_rows_tile(D, R);
     const int64_t rows = p.total_q * p.q_heads;
-    if (a.nsplit <= 16)
+    // a wave a row where splits are few or rows many (1280 rows, 32 splits: 19 us
+    // with attention, 27 with a workgroup a row; one row of 32 heads, 63 splits:
+    // a workgroup a row)
+    if (a.nsplit <= 16 || (a.nsplit <= 64 && rows >= 512))
         hipLaunchKernelGGL((qg::attn_join_kernel<T, D, R, TOK, 1>), dim3(static_cast<unsigned>(ceil_div(rows, 4))), dim3(256), 0, s, p);
     else
         hipLaunchKernelGGL((qg::attn_join_kernel<T, D, R, TOK, 4>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, p);

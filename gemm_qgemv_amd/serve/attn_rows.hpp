@@ -172,6 +172,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_rows_kernel(AttnParams p
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt)
             rows.template weigh<kMasked>(p, qt, x[qt], visible[qt], &s.co[1][0][0][hb * 32], 2 * kTok, top, base, g4);
+        // small groups of vector and matrix instructions in turn (2048 float32
+        // rows after 8192 cached tokens: 735 us, 750 without; with one product a
+        // piece, bfloat16, the compiler's own order is as good: 541 and 542)
+        if constexpr (kTwo) __builtin_amdgcn_iglp_opt(0);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             f16x8 ph[QT], pl[QT];
