@@ -11,8 +11,9 @@
 // in binary16, so nothing of the cache is rounded, and a float32 query or
 // weight goes as two binary16 pieces (22 bits) where a dequantized cache
 // would need three products of pieces. Scales and biases are applied in
-// float32 outside of them. The value codes are centred (z) so that the
-// accumulators hold sums that cancel no worse than the result does.
+// float32 outside of them. With float32 queries the codes of K and V are
+// centred (z), so that the accumulators hold sums that cancel no worse than the
+// result does.
 //
 // Operand layouts (v_mfma_f32_16x16x32_f16; l = lane, g4 = l / 16):
 //   scores   A = 16 tokens (row l % 16) x 32 channels, B = 32 channels x 16
@@ -24,8 +25,9 @@
 // lane's score results are its B operand of the second product as they are
 // (no exchange between lanes), and the nibbles of a dword are masked in
 // place: halves (n, n + 4) of a dword come out of one AND, as binary16
-// subnormals n * 2^-24 (K) or, with an OR and a packed add, as c - 8 (V); odd
-// nibbles come out 16 times too large, which the other operand makes good.
+// subnormals n * 2^-24 (bfloat16 queries) or, with an OR and a packed add, as
+// c - 8 (float32 queries); odd nibbles come out 16 times too large, which the
+// other operand makes good.
 // V's codes are stored token by token; ds_read_b64_tr_b4 transposes 16 x 16
 // nibbles among 16 lanes as it reads them.
 //

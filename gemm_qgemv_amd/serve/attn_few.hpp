@@ -6,6 +6,14 @@
 // registers one tile ahead and passed through LDS; with RW = 1 a wave passes
 // its own tile to itself and waits for no other. The KW partial results meet
 // in LDS at the end.
+//
+// 16 rows are the least a matrix instruction takes: with 4 query heads a
+// key/value head 12 columns are idle, and the vector work of a tile (600
+// instructions of 64 tokens at 128 channels in float32, half of them to make
+// operands of the codes) is the same for 1 row as for 16. 64 bfloat16 requests
+// of 1024 to 8192 tokens (360 MB): 86 us, 4.2 TB/s, all of it from one page 70,
+// so half memory, half the waves' own chains; one float32 request of 131071
+// (151 MB): 45 us, 3.3 TB/s, from one page 39: the chains, at two waves a SIMD.
 #pragma once
 
 #include "attn_common.hpp"

@@ -11,7 +11,9 @@ namespace qg {
 // statistics of the splits are taken a lane each; then runs of D / 4 lanes
 // add up the splits s = run, run + runs, ..., and the runs are added in a
 // fixed tree. The rows of a tile share their splits, so their count is found
-// from the row's tile as the attention kernels do.
+// from the row's tile as the attention kernels do. A chain of latencies (cu_q,
+// kv_len, statistics, partial results) of 4 to 6 us, whatever the sizes up to
+// some 10 MB of partial results; split counts are chosen with that in mind.
 constexpr int kMaxSplits = 256;
 
 template <typename T, int D, int R, int TOK, int WAVES>
