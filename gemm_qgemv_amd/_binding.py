@@ -104,9 +104,10 @@ def lib() -> ctypes.CDLL:
 def _ptr(t):
     if t is None:
         return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    try:                         # the common case first: a call passes up to 12 tensors
+        return t.data_ptr()
+    except AttributeError:
+        return t                 # an address
 
 
 _current_stream = None

@@ -79,8 +79,11 @@ int qkv_plan(const int32_t *len_old, const int32_t *keep, const int32_t *n_new, 
                      table_stride, ring, ring_size, state_in, state_out, kv_len, cu_q, slots, pos, total, denied};
     // two tokens a thread (each takes a chain of LDS reads to find its request;
     // every workgroup repeats the running sums; 65536 tokens of 512 requests: 13.3
-    // us at eight, 6.7 at two)
-    const auto grid = static_cast<unsigned>(std::clamp<int64_t>(ceil_div(total, qg::kPlanThreads * 2), 1, 256));
+    // us at eight, 6.7 at two); and a workgroup for eight requests, whose pages
+    // may all come back though they get few tokens (64 requests, four of them
+    // ended with some 1000 pages: 7.5 us with one workgroup, 4.2 with eight)
+    const int64_t parts = std::max(ceil_div(total, qg::kPlanThreads * 2), ceil_div(batch, 8));
+    const auto grid = static_cast<unsigned>(std::clamp<int64_t>(parts, 1, 256));
     const size_t lds = (3 * static_cast<size_t>(batch) + 1) * 4;
     static const bool allowed = [] {
         return hipFuncSetAttribute(reinterpret_cast<const void *>(qg::kv_plan_kernel),

@@ -1,9 +1,8 @@
 // plan.hpp -- pages, lengths, row starts and slots of a step, from lengths.
 //
-// A few thousand integer operations: the floor is one launch (6.4 us for 64
-// decoding requests and 6.6 for 512 with 65536 new tokens, calls back to
-// back, of which the host's part of a launch is 5; the rest is the chain of
-// loads: lengths, ring counts, ring entry). Every workgroup computes the
+// A few thousand integer operations: the floor is one launch (4.2 us for 64
+// decoding requests and 6.5 for 512 with 65536 new tokens, replayed from a
+// graph: a launch and a chain of loads, lengths, ring counts, ring entry). Every workgroup computes the
 // running sums over all requests itself (a few hundred cycles; the requests'
 // lengths come from L2) and then fills its share of the slots, of the pages
 // taken or of those given back (three rows of workgroups, so that the three
