@@ -12,12 +12,13 @@
 // that of the 64-bit keys argmax_key(x, index). A wave keeps its best 64 keys
 // sorted over its lanes; a block of 1024 logits is looked at for them only if
 // its maximum passes the last one wanted, which gets rare soon (for the n-th
-// block about top / n). The block's candidates, one a lane in rounds, are
-// sorted and merged into the list by bitonic networks over lanes (DPP and
-// permlane swaps: no LDS round trips).
+// block about top / n). The block's candidates, one a lane in rounds, are put
+// into the list one by one where they are few, or sorted and merged into it by
+// bitonic networks over lanes (DPP and permlane swaps: no LDS round trips).
 //
-// 1024 rows of 151936 logits (622 MB): 127 us, 4.9 TB/s, as fast as a copy's
-// reads go; one row: 15 us, two launches and their latencies (9 and 6 us).
+// 1024 rows of 151936 logits (622 MB), the best 5: 118.5 us, 5.25 TB/s, bound by
+// HBM; one row, the best 20: 13.2 us, 7.5 without alternatives: two launches and
+// the latencies of the networks.
 //
 // A row is cut into slices over workgroups, each slice into runs of blocks
 // over 4 waves; the parts are joined over LDS and, with more than one slice,
@@ -51,6 +52,10 @@ constexpr int kLpThreads = 256;
 constexpr int kLpWaves = kLpThreads / 64;
 constexpr int kLpQuads = 4;                          // 16-byte loads a lane has in flight
 constexpr int kLpBlock = 64 * 4 * kLpQuads;          // logits a wave takes at a time
+// Candidates of a round that are put into the list one by one; more are sorted
+// and merged (27 exchange steps). 1024 rows of 151936, the best 32: 147 us with 8,
+// 150 with 4, 148 with 16, 181 with none.
+constexpr int kLpFew = 8;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -102,7 +107,7 @@ __device__ __forceinline__ uint64_t exchange(uint64_t k, bool keep_max)
 }
 
 // One run of exchange steps W / 2, .., 1 of a bitonic network over the 64
-// lanes; lanes of runs of W in turn sort up and down (W = 64: all down).
+// lanes; lanes of runs of W in turn sort down and up (W = 64: all down).
 template <int W, int D>
 __device__ __forceinline__ uint64_t bitonic_steps(uint64_t k, int lane)
 {
@@ -125,11 +130,10 @@ __device__ __forceinline__ uint64_t bitonic_sort(uint64_t k, int lane)
     return bitonic_steps<64, 32>(k, lane);
 }
 
-// The 64 largest of two descending lists, descending.
-__device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b, int lane)
+// The 64 largest of a descending and an ascending list, descending.
+__device__ __forceinline__ uint64_t merge_lists(uint64_t down, uint64_t up, int lane)
 {
-    const uint64_t r = shfl_xor_u64(b, 63);          // reversed
-    return bitonic_steps<64, 32>(a > r ? a : r, lane);
+    return bitonic_steps<64, 32>(down > up ? down : up, lane);
 }
 
 __device__ __forceinline__ uint64_t lane_u64(uint64_t v, int src)
@@ -139,10 +143,27 @@ __device__ __forceinline__ uint64_t lane_u64(uint64_t v, int src)
     return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 
+// A key put into its place in a descending list (the last one falls out).
+__device__ __forceinline__ uint64_t insert_key(uint64_t list, uint64_t key, int lane)
+{
+    const int place = __popcll(__ballot(list > key));
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<uint32_t>(list), 0x138, 0xF, 0xF, false);          // lane - 1's
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<uint32_t>(list >> 32), 0x138, 0xF, 0xF, false);
+    const uint64_t before = (static_cast<uint64_t>(hi) << 32) | lo;
+    return lane < place ? list : lane == place ? key : before;
+}
+
 __device__ __forceinline__ float key_value(uint64_t key)
 {
     const uint32_t u = static_cast<uint32_t>(key >> 32);
     return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
+
+// Joined with lane ^ d's; both partners add in the same order.
+__device__ __forceinline__ void lp_join_lanes(Moments &mo, int lane, int d)
+{
+    const Moments o = {lane_xor_f32(mo.m, d), lane_xor_f32(mo.z, d), lane_xor_f32(mo.t, d)};
+    mo = lane & d ? lp_join(o, mo) : lp_join(mo, o);
 }
 
 struct RowResult {
@@ -165,20 +186,21 @@ __device__ __forceinline__ RowResult lp_join_waves(RowResult r, bool want_top)
         for (int n = WAVES / 2; n >= 1; n >>= 1) {
             if (wave >= n && wave < 2 * n) lists[wave][lane] = r.list;
             __syncthreads();
-            if (wave < n) r.list = merge_lists(r.list, lists[wave + n][lane], lane);
+            if (wave < n) r.list = merge_lists(r.list, lists[wave + n][63 - lane], lane);
         }
     } else {
         __syncthreads();
     }
+    // a wave's statistics in a lane, joined by halves (every lane gets them)
+    const f32x4 mine = stat[lane & (WAVES - 1)];
     RowResult o;
-    o.mo = {kLowest, 0.0f, 0.0f};
-    o.before = 0;
+    o.mo = {mine[0], mine[1], mine[2]};
+    o.before = __float_as_int(mine[3]);
     o.list = r.list;
-#pragma unroll 4
-    for (int w = 0; w < WAVES; ++w) {
-        const f32x4 s = stat[w];
-        o.mo = lp_join(o.mo, {s[0], s[1], s[2]});
-        o.before += __float_as_int(s[3]);
+#pragma unroll
+    for (int d = WAVES / 2; d >= 1; d >>= 1) {
+        lp_join_lanes(o.mo, lane, d);
+        o.before += __float_as_int(lane_xor_f32(__int_as_float(o.before), d));
     }
     return o;
 }
@@ -319,11 +341,21 @@ __global__ __launch_bounds__(kLpThreads) void logprob_kernel(LogprobParams p)
                 const uint32_t index = static_cast<uint32_t>(at(slot >> 2) + (slot & 3));
                 const uint64_t key = best ? (static_cast<uint64_t>(best) << 32) | (0xFFFFFFFFu - index) : 0;
                 const bool passes = key > last_key;
-                if (!__any(passes)) break;
+                uint64_t in = __ballot(passes);
+                if (in == 0) break;
 #pragma unroll
                 for (int n = 0; n < 4 * kLpQuads; ++n) order[n] = n == slot ? 0 : order[n];
-                r.list = merge_lists(r.list, bitonic_sort(passes ? key : 0, lane), lane);
-                last_key = lane_u64(r.list, top - 1);
+                if (__popcll(in) > kLpFew) {
+                    r.list = merge_lists(r.list, shfl_xor_u64(bitonic_sort(passes ? key : 0, lane), 63), lane);
+                    last_key = lane_u64(r.list, top - 1);
+                } else {
+                    for (; in != 0; in &= in - 1) {
+                        const uint64_t k = lane_u64(key, __builtin_ctzll(in));
+                        if (k <= last_key) continue;             // an earlier one has raised the bar
+                        r.list = insert_key(r.list, k, lane);
+                        last_key = lane_u64(r.list, top - 1);
+                    }
+                }
                 last = key_value(last_key);
             }
         }
@@ -331,11 +363,7 @@ __global__ __launch_bounds__(kLpThreads) void logprob_kernel(LogprobParams p)
 
     // lanes joined
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-        const Moments o = {lane_xor_f32(r.mo.m, d), lane_xor_f32(r.mo.z, d), lane_xor_f32(r.mo.t, d)};
-        // both partners add in the same order
-        r.mo = lane & d ? lp_join(o, r.mo) : lp_join(r.mo, o);
-    }
+    for (int d = 32; d >= 1; d >>= 1) lp_join_lanes(r.mo, lane, d);
     r = lp_join_waves<kLpWaves>(r, top > 0);
     if (p.nslice == 1) {
         lp_finish(p, row, r);
@@ -357,13 +385,25 @@ __global__ __launch_bounds__(kLpJoinThreads) void logprob_join_kernel(LogprobPar
     r.mo = {kLowest, 0.0f, 0.0f};
     r.before = 0;
     r.list = 0;
-    for (int s = wave; s < p.nslice; s += kWaves) {
-        const int64_t at = row * p.nslice + s;
-        const f32x4 v = p.part[at];
-        const uint64_t list = lane < p.top ? p.part_keys[at * p.top + lane] : 0;
-        r.mo = lp_join(r.mo, {v[0], v[1], v[2]});
-        r.before += __float_as_int(v[3]);
-        if (p.top > 0) r.list = merge_lists(r.list, list, lane);
+    // a few slices' results are asked for before the first is used
+    constexpr int kAhead = 4;
+    for (int s0 = wave; s0 < p.nslice; s0 += kWaves * kAhead) {
+        f32x4 v[kAhead];
+        uint64_t list[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int s = s0 + j * kWaves;
+            const int64_t at = row * p.nslice + (s < p.nslice ? s : s0);
+            v[j] = p.part[at];
+            list[j] = 63 - lane < p.top ? p.part_keys[at * p.top + 63 - lane] : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (s0 + j * kWaves >= p.nslice) break;
+            r.mo = lp_join(r.mo, {v[j][0], v[j][1], v[j][2]});
+            r.before += __float_as_int(v[j][3]);
+            if (p.top > 0) r.list = merge_lists(r.list, list[j], lane);
+        }
     }
     r = lp_join_waves<kWaves>(r, p.top > 0);
     lp_finish(p, row, r);
