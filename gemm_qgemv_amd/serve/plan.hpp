@@ -1,16 +1,16 @@
 // plan.hpp -- pages, lengths, row starts and slots of a step, from lengths.
 //
-// A few thousand integer operations: the floor is one launch (4.2 us for 64
-// decoding requests and 6.5 for 512 with 65536 new tokens, replayed from a
-// graph: a launch and a chain of loads, lengths, ring counts, ring entry). Every workgroup computes the
-// running sums over all requests itself (a few hundred cycles; the requests'
-// lengths come from L2) and then fills its share of the slots, of the pages
-// taken or of those given back (three rows of workgroups, so that the three
-// latencies do not add up). So there is one launch, no workspace, and nothing
-// for one workgroup to wait for in another. That needs two rules of the
-// operator: pages given back in a call are not taken in the same call
-// (takers read ring entries head..tail-1, givers write from tail on), and
-// the new ring counts go to another place than the old ones.
+// A few thousand integer operations: the floor is one launch (4.1 us for 64
+// decoding requests and 6.4 for 512 with 65536 new tokens, replayed from a
+// graph: a launch and a chain of loads, lengths, ring counts, ring entry).
+// Every workgroup computes the running sums over all requests itself (a few
+// hundred cycles; the requests' lengths come from L2) and then fills its share
+// of the slots, of the pages taken or of those given back (three rows of
+// workgroups, so that the three latencies do not add up). So there is one
+// launch, no workspace, and nothing for one workgroup to wait for in another.
+// That needs two rules of the operator: pages given back in a call are not
+// taken in the same call (takers read ring entries head..tail-1, givers write
+// from tail on), and the new ring counts go to another place than the old ones.
 #pragma once
 
 #include <hip/hip_runtime.h>
