@@ -98,11 +98,7 @@ int check_attn_sizes(const qg_kv_cache &c, int batch, int64_t total_q, int64_t m
 template <auto KERNEL>
 void launch_with_lds(size_t lds, dim3 grid, const qg::AttnParams &p, hipStream_t s)
 {
-    static const bool allowed = [&] {
-        return hipFuncSetAttribute(reinterpret_cast<const void *>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                   static_cast<int>(lds)) == hipSuccess;
-    }();
-    (void)allowed;
+    allow_lds<KERNEL>(lds);
     hipLaunchKernelGGL(KERNEL, grid, dim3(qg::kAttnThreads), lds, s, p);
 }
 

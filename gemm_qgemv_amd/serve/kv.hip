@@ -85,11 +85,7 @@ int qkv_plan(const int32_t *len_old, const int32_t *keep, const int32_t *n_new, 
     const int64_t parts = std::max(ceil_div(total, qg::kPlanThreads * 2), ceil_div(batch, 8));
     const auto grid = static_cast<unsigned>(std::clamp<int64_t>(parts, 1, 256));
     const size_t lds = (3 * static_cast<size_t>(batch) + 1) * 4;
-    static const bool allowed = [] {
-        return hipFuncSetAttribute(reinterpret_cast<const void *>(qg::kv_plan_kernel),
-                                   hipFuncAttributeMaxDynamicSharedMemorySize, (3 * QG_MAX_PLAN_BATCH + 1) * 4) == hipSuccess;
-    }();
-    (void)allowed;
+    allow_lds<qg::kv_plan_kernel>((3 * QG_MAX_PLAN_BATCH + 1) * 4);
     hipLaunchKernelGGL(qg::kv_plan_kernel, dim3(grid, 3), dim3(qg::kPlanThreads), lds, stream, p);
     return launch_status();
 }

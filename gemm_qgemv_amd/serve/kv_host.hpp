@@ -2,6 +2,8 @@
 // shared by the entry points that take one.
 #pragma once
 
+#include <atomic>
+
 #include "../csrc/host_args.hpp"
 #include "kv_cache.hpp"
 
@@ -45,6 +47,21 @@ namespace {
     v.dim = c.head_dim;
     v.dim_shift = __builtin_ctz(static_cast<unsigned>(c.head_dim));
     return v;
+}
+
+// Lets a kernel be launched with up to `bytes` of dynamic LDS: asked for on
+// its first call on a device (where it is refused, so is the launch).
+template <auto KERNEL>
+[[maybe_unused]] void allow_lds(size_t bytes)
+{
+    static std::atomic<uint64_t> asked{0};
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (asked.load(std::memory_order_relaxed) & bit) return;
+    if (hipFuncSetAttribute(reinterpret_cast<const void *>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            static_cast<int>(bytes)) == hipSuccess)
+        asked.fetch_or(bit, std::memory_order_relaxed);
 }
 
 }  // namespace
