@@ -2,7 +2,7 @@
 // cache, and the values of slots read back.
 //
 // A group of 64 channels is held by 8 lanes of 8 values: minimum and maximum
-// by DPP over the 8 lanes, scale = bf16((max - min) / 15), bias = bf16(min),
+// by DPP over the 8 lanes, scale = bf16((max - min) * (1 / 15)), bias = bf16(min),
 // code = round_half_even((x - bias) / scale) into 0..15 (I Built an LLM
 // Inference Engine on a 15 year old GPU..., "Quantization: The Model Doesn't
 // Run on INT4": the scale is the range over 15, the minimum is kept). A lane
@@ -57,6 +57,10 @@ __device__ __forceinline__ float reduce8(float v)
     return step(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, false)));
 }
 
+// The scale is the range times this, one operation where a division takes 10;
+// the product is off by at most one bit of 24 before it is rounded to 8.
+constexpr float kFifteenth = 1.0f / 15.0f;
+
 // A group of 64 values (8 lanes of 8) as bf16 bits of scale and bias (low and
 // high half of `coef`) and this lane's 8 codes.
 __device__ __forceinline__ void quantize_group(const float (&x)[8], int lane, uint32_t &codes, uint32_t &coef)
@@ -72,7 +76,7 @@ __device__ __forceinline__ void quantize_group(const float (&x)[8], int lane, ui
     lo = reduce8<false>(lo);
     hi = reduce8<true>(hi);
     const uint64_t ok = __ballot(largest < 0x7f800000u);
-    const uint32_t both = f32_to_bf16_pair((hi - lo) / 15.0f, lo);
+    const uint32_t both = f32_to_bf16_pair((hi - lo) * kFifteenth, lo);
     uint32_t sb = both & 0xffffu, bb = both >> 16;
     const bool good = ((ok >> (lane & 56)) & 0xff) == 0xff && (sb & 0x7f80u) != 0x7f80u && (bb & 0x7f80u) != 0x7f80u;
     if ((sb & 0x7f80u) == 0) sb = 0;              // below the least normal: the group is its minimum

@@ -375,7 +375,8 @@ int qkv_plan(const int32_t *len_old, const int32_t *keep, const int32_t *n_new, 
  *   slots  int32 [n]; a token whose slot is outside the cache is skipped.
  *          Two tokens with one slot leave either token's bytes, mixed.
  * Each group x[0..63] is stored as
- *   scale = bf16((max x - min x) / 15), bias = bf16(min x)   (nearest even)
+ *   scale = bf16((max x - min x) * f), bias = bf16(min x)   (nearest even),
+ *   f the float32 nearest 1/15,
  *   code  = round_half_even((x - bias) / scale), into 0..15,
  * in float32 arithmetic. A scale below 2^-126 is stored as 0 with codes 0
  * (the group is its minimum); where scale or bias is not finite (a group

@@ -33,7 +33,7 @@ def quantize(x):
     if not np.all(np.isfinite(x)):
         return np.zeros(64, np.uint8), 0x7FC0, 0x7FC0
     with np.errstate(over="ignore"):
-        s_bits = int(bf16_bits(np.float32(np.float32(x.max() - x.min()) / np.float32(15)))[0])
+        s_bits = int(bf16_bits(np.float32(np.float32(x.max() - x.min()) * np.float32(1 / 15)))[0])
         b_bits = int(bf16_bits(np.float32(x.min()))[0])
     if (s_bits & 0x7F80) == 0x7F80 or (b_bits & 0x7F80) == 0x7F80:
         return np.zeros(64, np.uint8), 0x7FC0, 0x7FC0
