@@ -211,6 +211,28 @@ def test_append_and_read(torch, dtype, n, H, D, page, pad):
         assert np.array_equal(got[:, :H * D], w, equal_nan=True)
 
 
+def test_append_scales_between_bf16_numbers(torch):
+    """Ranges of 15 times the middle of two bf16 numbers: the product with 1/15
+    may lie on either side of the middle, and decides."""
+    rng = np.random.default_rng(15)
+    n, page = 512, 64
+    middle = (256 + np.arange(1, 256, 2)) / 256.0                          # 9 significant bits, the last one set
+    x = rng.random((n, 64)).astype(np.float32)
+    x[:, 0], x[:, 63] = 0.0, np.tile(15 * middle, 4) * np.repeat(2.0 ** np.array([-9, -1, 0, 20]), 128)
+    x[:, 1:63] *= x[:, 63:]
+    cache = q.KVCache(torch.zeros(n // page * ref.block_bytes(page, 64), dtype=torch.uint8, device="cuda"), n // page, page, 1, 64)
+    t, slots = dev(torch, x), np.arange(n, dtype=np.int32)
+    q.qkv_append(q.QG_F32, t, 64, t, 64, dev(torch, slots), n, cache)
+    torch.cuda.synchronize()
+    data = cache.data.cpu().numpy().reshape(n // page, 1, -1)
+    want = np.zeros_like(data)
+    ref.append(want, page, 1, 64, x, x, slots)
+    assert np.array_equal(data, want)
+    _, mid, end = ref.parts(page, 64, 0)
+    scales = np.ascontiguousarray(data[:, 0, mid:end]).view("<u2")[:, ::2].reshape(-1)
+    assert np.array_equal(scales, (t[:, 63] / 15.0).bfloat16().view(torch.int16).cpu().numpy().view(np.uint16))
+
+
 def test_append_slots_past_2_gib(torch):
     """A cache of 4.8 GB: byte offsets past 32 bits, the last slot included."""
     page, H, D = 256, 8, 256
