@@ -8,8 +8,8 @@
 // Run on INT4": the scale is the range over 15, the minimum is kept). A lane
 // then stores its 8 codes as one dword: 8 lanes write a group's 32 bytes.
 // Bound by HBM at a prompt's sizes, with the vector unit close behind for
-// append (16411 tokens of 8 heads of 128 bfloat16 channels: 86 MB in 21 us,
-// 4.1 TB/s, vector unit 80% busy; read back as float32 153 MB in 30.5 us, 5.0
+// append (16411 tokens of 8 heads of 128 bfloat16 channels: 86 MB in 20 us,
+// 4.3 TB/s, vector unit 77% busy; read back as float32 153 MB in 30.7 us, 5.0
 // TB/s), by latency at a decode step's (64 tokens 3.1 and 2.7 us).
 #pragma once
 
