@@ -134,8 +134,9 @@ __device__ __forceinline__ bool find_tile(const AttnParams &p, int64_t slot, Row
     t.b = count - 1;
     t.q0 = attn_cu(p, t.b);
     t.n_q = attn_cu(p, t.b + 1) - t.q0;
+    // row starts that are not in order can make `b` a request that starts behind this slot
     const int64_t row0 = (slot - tile_start<R>(p, t.b)) * R;
-    if (t.n_q <= 0 || row0 >= int64_t(t.n_q) * p.group) return false;
+    if (t.n_q <= 0 || row0 < 0 || row0 >= int64_t(t.n_q) * p.group) return false;
     tile_tokens(p, t, row0, R);
     return true;
 }

@@ -42,7 +42,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p)
     t.b = count - 1;
     t.q0 = attn_cu(p, t.b);
     t.n_q = attn_cu(p, t.b + 1) - t.q0;
-    if (tok - t.q0 >= t.n_q) return;
+    if (tok < t.q0 || tok - t.q0 >= t.n_q) return;
     const int64_t r = (tok - t.q0) * p.group + head % p.group;
     tile_tokens(p, t, r / R * R, R);
     const int32_t from = t.lo / TOK * TOK;

@@ -423,7 +423,8 @@ int qkv_read(int dtype, const qg_kv_cache *cache, const int32_t *slots, int64_t 
  * and lse -infinity. Contents out of range: a request with kv_len > max_kv,
  * and rows that see a page number outside the cache, give NaN; kv_len < 0 is
  * 0; rows outside [0, total_q) do not exist, and rows of no request are not
- * written. What masked places hold (codes or coefficients of tokens a row
+ * written; where the starts in cu_q are not in order, the rows from the
+ * least to the largest of them may hold anything. What masked places hold (codes or coefficients of tokens a row
  * does not see, NaN and infinities among them) does not matter.
  *   1 <= batch <= 65535, 1 <= total_q <= 2^31 - 1, 1 <= max_q, 1 <= max_kv
  *   <= 2^30, q_heads a multiple of kv_heads, q_heads <= 1024, scale finite
