@@ -82,9 +82,10 @@ constexpr float kHead = 7.0f, kSlack = 7.0f;
 struct RowTile {
     int b;
     int32_t q0;           // first query row of the request in the batch
-    int32_t n_q, kv;      // its new tokens and its tokens
+    int32_t n_q, kv;      // its new tokens that have rows, and its tokens
+    int32_t before;       // tokens before its first row's (below 0: that many rows see none)
     int64_t row0, rows;
-    int32_t first, last;  // tokens of its first and its last row (below 0: before the request)
+    int32_t first, last;  // tokens of the tile's first and last row (below 0: before the request)
     int32_t lo, hi;
     bool poison;          // longer than the call allows
 };
@@ -109,11 +110,14 @@ __device__ __forceinline__ void tile_tokens(const AttnParams &p, RowTile &t, int
     t.kv = p.kv_len[t.b] < 0 ? 0 : p.kv_len[t.b];
     t.poison = t.kv > p.max_kv;
     if (t.poison) t.kv = 0;
+    // counted from the request's own end: rows behind total_q do not exist, but their tokens do
+    const int64_t before = int64_t(t.kv) - (int64_t(p.cu_q[t.b + 1]) - t.q0);
+    t.before = static_cast<int32_t>(before < -INT32_MAX ? -INT32_MAX : before);
     t.row0 = row0;
     t.rows = int64_t(t.n_q) * p.group;
     const int64_t last = row0 + R < t.rows ? row0 + R : t.rows;
-    t.first = t.kv - t.n_q + static_cast<int32_t>(row0 / p.group);
-    t.last = t.kv - t.n_q + static_cast<int32_t>((last - 1) / p.group);
+    t.first = t.before + static_cast<int32_t>(row0 / p.group);
+    t.last = t.before + static_cast<int32_t>((last - 1) / p.group);
     t.hi = t.last < 0 ? 0 : t.last + 1;
     const int64_t lo = p.window > 0 ? int64_t(t.first) - p.window + 1 : 0;
     t.lo = lo < 0 ? 0 : lo < t.hi ? static_cast<int32_t>(lo) : t.hi;
@@ -243,7 +247,7 @@ struct QueryRows {
     static constexpr float kUnit = kTwo ? 1.0f : 5.9604644775390625e-08f;       // of a code as the matrix cores see it
     f16x8 qh[QT][NG][2], ql[kTwo ? QT : 1][NG][2];
     float qsum[QT][NG], factor[QT];
-    int32_t pos[QT];                                       // the row's token, -1 for no row
+    int32_t pos[QT];                                       // the row's token, -1 for no row or none
     f32x4 acc[QT][D / 16];
     float ref[QT], total[QT], bias[QT][NG];
 
@@ -256,7 +260,7 @@ struct QueryRows {
             const bool live = row < t.rows;
             const int32_t tok = live ? static_cast<int32_t>(row / p.group) : 0;
             const int head = kv_head * p.group + (live ? static_cast<int>(row - int64_t(tok) * p.group) : 0);
-            pos[qt] = live ? t.kv - t.n_q + tok : -1;
+            pos[qt] = live ? max(t.before + tok, -1) : -1;
             const T *src = static_cast<const T *>(p.q) + int64_t(t.q0 + tok) * p.q_stride + int64_t(head) * D;
             float x[NG][2][8];
             float top = 0.0f;

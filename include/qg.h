@@ -422,7 +422,9 @@ int qkv_read(int dtype, const qg_kv_cache *cache, const int32_t *slots, int64_t 
  * A row that sees no token (kv_len 0, or fewer tokens than rows) gives out 0
  * and lse -infinity. Contents out of range: a request with kv_len > max_kv,
  * and rows that see a page number outside the cache, give NaN; kv_len < 0 is
- * 0; rows outside [0, total_q) do not exist, and rows of no request are not
+ * 0; rows outside [0, total_q) do not exist (the others of their request keep
+ * their tokens: a call may have fewer rows than the plan that made cu_q), and
+ * rows of no request are not
  * written; where the starts in cu_q are not in order, the rows from the
  * least to the largest of them may hold anything. What masked places hold (codes or coefficients of tokens a row
  * does not see, NaN and infinities among them) does not matter.

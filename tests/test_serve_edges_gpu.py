@@ -35,3 +35,20 @@ def test_attention_row_starts_out_of_order(torch, cu, G, D, kv, max_q):
     inside = [min(max(s, 0), c.total) for s in cu]
     for lo, hi in ((0, min(inside)), (max(inside), c.total)):
         assert np.all(out[lo:hi] == 77) and np.all(lse[lo:hi] == 77)
+
+
+@pytest.mark.parametrize("G,D,lens,cut", [(2, 64, [(40, 6), (30, 5)], 8), (8, 128, [(90, 3), (70, 40)], 25), (4, 64, [(1500, 3)], 2),
+                                          (3, 256, [(60, 30)], 11), (24, 64, [(20, 1), (300, 100)], 61)])
+@pytest.mark.parametrize("window", [0, 9])
+def test_attention_rows_cut_off(torch, G, D, lens, cut, window):
+    """A call with fewer rows than cu_q counts: the rows that exist stand for
+    the same tokens as in the whole call."""
+    say("cut off", G, D, lens, cut, window)
+    c = AttnCase(torch, "f32", 1, G, D, 16, lens, window=window)
+    o, l, spread, amp = c.want()
+    c.total, c.q = cut, c.q[:cut].contiguous()
+    out, lse = c.run()
+    kv = float(c.kv_len.max())
+    tol = spread * (2.0 ** -21 * 2 * (1 + amp[..., None]) + 2.0 ** -24 * (kv / 16 + 16))
+    assert np.all(np.abs(out - o[:cut]) <= tol[:cut])
+    assert np.all(np.abs(lse - l[:cut]) <= 2.0 ** -20 * (1 + amp[:cut]) + 2.0 ** -22 * np.abs(l[:cut]))
