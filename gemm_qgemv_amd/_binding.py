@@ -107,7 +107,9 @@ def _ptr(t):
     try:                         # the common case first: a call passes up to 12 tensors
         return t.data_ptr()
     except AttributeError:
-        return t                 # an address
+        if isinstance(t, int):   # an address
+            return t
+        raise TypeError(f"a tensor or a device address is needed, not {type(t).__name__}") from None
 
 
 _current_stream = None

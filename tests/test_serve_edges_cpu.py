@@ -1,0 +1,31 @@
+"""Arguments of the binding and of the entry points at their edges; no call
+here reaches a GPU (see test_serve_abi_cpu.py)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import gemm_qgemv_amd as q
+from test_serve_abi_cpu import LP, PLAN, at, cache
+
+
+@pytest.mark.parametrize("host", [b"abc", "abc", bytearray(64), (ctypes.c_float * 16)(), np.zeros(16, np.float32), 1.5, [1, 2]])
+def test_only_tensors_and_addresses_are_taken_as_device_memory(host):
+    """What has no device pointer is refused; ctypes would pass the host
+    address of some of these on."""
+    c = cache()
+    calls = [(q.qgemv, (q.QG_U4_G64, host, at(1), at(2), at(3), at(4), 64, 64, 1)),
+             (q.qgemm, (q.QG_I8_ROW, at(1), at(2), None, host, at(4), 64, 64, 1)),
+             (q.qgemv_argmax_noalloc, (q.QG_U4_G64, at(1), at(2), at(3), host, None, at(5), 64, 64, 1)),
+             (q.qembed, (q.QG_U4_G64, at(1), at(2), at(3), host, at(4), 64, 64, 1)),
+             (q.qkv_append, (q.QG_F32, host, 128, at(2), 128, at(3), 4, c)),
+             (q.qkv_read, (q.QG_F32, c, at(3), 4, at(1), 128, host, 128))]
+    for fn, args in calls:
+        with pytest.raises(TypeError):
+            fn(*args, stream=0)
+    with pytest.raises(TypeError):
+        q.qkv_plan(**dict(PLAN, slots=host), stream=0)
+    with pytest.raises(TypeError):
+        q.qlogprobs(**dict(LP, logits=host), stream=0)
+    with pytest.raises(TypeError):
+        q.KVCache(host, 8, 16, 2, 64)
