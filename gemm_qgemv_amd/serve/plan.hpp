@@ -235,7 +235,8 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(PlanParams p)
                 const int64_t col = at_pos >> p.page_shift;
                 const int64_t page = col < r.have ? p.table[b * p.table_stride + col]
                                                   : p.ring[ring_at(front, take_at[b] + (col - r.have))];
-                slot = static_cast<int32_t>(page * (int64_t(1) << p.page_shift) + (at_pos & ((int64_t(1) << p.page_shift) - 1)));
+                const int64_t place = page * (int64_t(1) << p.page_shift) + (at_pos & ((int64_t(1) << p.page_shift) - 1));
+                if (place == static_cast<int32_t>(place)) slot = static_cast<int32_t>(place);    // or it would be another page's
             }
         }
         p.slots[t] = slot;

@@ -349,7 +349,8 @@ size_t qkv_cache_bytes(const qg_kv_cache *cache);
  *   cu_q         int32 [batch+1]  running sums of n_new (denied requests
  *                included: their rows exist and are void)
  *   slots, pos   int32 [total]    slot and position of each new token, in
- *                request order; slot -1 for the tokens of a denied request;
+ *                request order; slot -1 for the tokens of a denied request
+ *                and where the slot (page * page_size + place) is no int32;
  *                both -1 behind the last token (total may be larger, as
  *                under graph capture; tokens behind total are dropped)
  *   denied       int32 [1]        how many requests were denied

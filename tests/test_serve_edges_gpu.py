@@ -52,3 +52,31 @@ def test_attention_rows_cut_off(torch, G, D, lens, cut, window):
     tol = spread * (2.0 ** -21 * 2 * (1 + amp[..., None]) + 2.0 ** -24 * (kv / 16 + 16))
     assert np.all(np.abs(out - o[:cut]) <= tol[:cut])
     assert np.all(np.abs(lse - l[:cut]) <= 2.0 ** -20 * (1 + amp[:cut]) + 2.0 ** -22 * np.abs(l[:cut]))
+
+
+# --- the page plan -----------------------------------------------------------------
+
+@pytest.mark.parametrize("page,number", [(16, 1 << 28), (1 << 20, 4096), (16, (1 << 28) + 1), (1 << 20, 2047), (256, 2 ** 31 - 1),
+                                         (16, -(1 << 28)), (1 << 20, -2048), (4, -3)])
+def test_plan_slots_past_32_bits(torch, page, number):
+    """A page whose slots are no 32-bit numbers, in the table and in the ring:
+    its tokens get slot -1, never the slot of another page."""
+    say("plan slots", page, number)
+    i32 = np.int32
+    table = Guarded(torch, 4, torch.int32)
+    table.t.copy_(dev(torch, np.array([number, -1, 5, -1], i32)))
+    ring = dev(torch, np.array([number, 7], i32))
+    o = {n: Guarded(torch, k, torch.int32) for n, k in (("kv_len", 2), ("cu_q", 3), ("slots", 6), ("pos", 6), ("denied", 1))}
+    state_out = torch.zeros(2, dtype=torch.int64, device="cuda")
+    q.qkv_plan(dev(torch, np.array([page - 2, page - 1], i32)), dev(torch, np.array([page - 2, page - 1], i32)),
+               dev(torch, np.array([1, 3], i32)), 2, page, table.t, 2, ring, 2, torch.tensor([0, 2], device="cuda"), state_out,
+               o["kv_len"].t, o["cu_q"].t, o["slots"].t, o["pos"].t, 6, o["denied"].t)
+    torch.cuda.synchronize()
+
+    def slot(number, at):
+        v = number * page + at
+        return v if -2 ** 31 <= v < 2 ** 31 else -1
+    assert table.numpy().tolist() == [number, -1, 5, number]
+    assert o["slots"].numpy().tolist() == [slot(number, page - 2), slot(5, page - 1), slot(number, 0), slot(number, 1), -1, -1]
+    assert o["pos"].numpy().tolist() == [page - 2, page - 1, page, page + 1, -1, -1]
+    assert o["denied"].numpy().tolist() == [0] and state_out.tolist() == [1, 2]
