@@ -171,7 +171,7 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(PlanParams p)
         else ++denied;
         if (first_block) {
             p.cu_q[b] = saturate(rows);
-            p.kv_len[b] = r.keep + (granted ? r.n_new : 0);
+            p.kv_len[b] = saturate(int64_t(r.keep) + (granted ? r.n_new : 0));
         }
         rows += r.n_new;
         grow += r.grow;

@@ -356,7 +356,7 @@ size_t qkv_cache_bytes(const qg_kv_cache *cache);
  *   denied       int32 [1]        how many requests were denied
  * state_in and state_out are distinct, so that a step can be planned again.
  * Contents out of range: len_old, keep and n_new are taken into
- * [0, 2^30], keep into [0, len_old]; a negative ring count is no free page;
+ * [0, 2^30], keep into [0, len_old], sums past 2^31 - 1 are 2^31 - 1; a negative ring count is no free page;
  * pages of a request behind table_stride are neither read nor given back;
  * page numbers pass through as they are.
  *   1 <= batch <= QG_MAX_PLAN_BATCH, 0 <= total, table_stride >= 1,

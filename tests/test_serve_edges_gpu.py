@@ -80,3 +80,22 @@ def test_plan_slots_past_32_bits(torch, page, number):
     assert o["slots"].numpy().tolist() == [slot(number, page - 2), slot(5, page - 1), slot(number, 0), slot(number, 1), -1, -1]
     assert o["pos"].numpy().tolist() == [page - 2, page - 1, page, page + 1, -1, -1]
     assert o["denied"].numpy().tolist() == [0] and state_out.tolist() == [1, 2]
+
+
+def test_plan_length_past_32_bits(torch):
+    """The longest length kept and the most new tokens: their sum is no int32
+    and is the largest one instead, as the row starts are."""
+    page, width, most = 1 << 20, 2048, 1 << 30
+    table = torch.arange(2 * width, dtype=torch.int32, device="cuda")
+    ring = torch.arange(width, dtype=torch.int32, device="cuda") + 2 * width
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")     # noqa: E731
+    kv_len, cu, slots, pos, denied = ints(0, 0), ints(0, 0, 0), ints(9, 9), ints(9, 9), ints(9)
+    state_out = torch.zeros(2, dtype=torch.int64, device="cuda")
+    q.qkv_plan(ints(most, 5), ints(most, 5), ints(most, most), 2, page, table, width, ring, width, torch.tensor([0, width], device="cuda"),
+               state_out, kv_len, cu, slots, pos, 2, denied)
+    torch.cuda.synchronize()
+    # request 0 goes from 1024 to 2048 pages, request 1 from 1 to 1025: all that are free
+    assert kv_len.tolist() == [2 ** 31 - 1, most + 5] and cu.tolist() == [0, most, 2 ** 31 - 1] and denied.tolist() == [0]
+    assert state_out.tolist() == [width, width] and pos.tolist() == [most, most + 1]
+    assert table[1024:2048].tolist() == ring[:1024].tolist()
+    assert table[2049:3073].tolist() == ring[1024:].tolist()
