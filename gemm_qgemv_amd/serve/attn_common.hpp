@@ -72,10 +72,46 @@ struct AttnParams {
 
 constexpr int kAttnThreads = 256;
 constexpr float kNoReference = -1e30f;   // below every score; finite, so that differences stay defined
-// A weight times a value scale stays below 2^(kHead + kSlack) in binary16;
-// the reference moves only when a score passes it by kSlack, so the
-// accumulators are rarely rescaled.
-constexpr float kHead = 7.0f, kSlack = 7.0f;
+// The weights' products with the value scales are binary16 operands, which hold
+// 2^-24 to 2^16. Tiles of tokens are taken in one of two ways.
+//
+// Plain tiles: every row sees all of their tokens, and their value scales lie in
+// one range, 2^(E - kRange) to 2^E for an exponent E of the workgroup. A row's
+// reference is 2^-kHead below its largest score times 2^E and moves only when
+// that passes it by kSlack, so the accumulators are rarely rescaled: products
+// stay below 2^(kHead + kSlack), and every channel group's largest one is at
+// least 1 (an odd token's a 16th of it) and keeps its 21 bits. They are taken as
+// they are.
+//
+// Careful tiles, all others: every row and group brings its products into the
+// range by a power of two of its own, that of the tile's largest, and undoes it on
+// the sums (about twice the vector work). They move the reference by the smallest
+// scale, so that no group's products in other tiles are lost below it, unless some
+// weight times its value would pass 2^(kApart + kHead + kSlack); and by what the
+// row itself sees, so that nothing masked, and no other row, changes it. One that is
+// careful for its scales alone sets E anew, kAbove above its largest one's.
+//
+// The sizes of values move a reference by 2^kSmallest to 2^kLargest at most:
+// weights, their sums and those of the values stay inside of float32.
+constexpr float kHead = 9.0f, kSlack = 5.0f;
+constexpr int kRange = 9, kAbove = 2, kApart = 70, kSmallest = -50, kLargest = 60;
+static_assert(kRange <= kHead, "a group's largest product in a plain tile is at least 2^(kHead - kRange)");
+
+// The e of a positive v in [2^(e-1), 2^e).
+__device__ __forceinline__ int float_exponent(float v) { return static_cast<int>((__float_as_uint(v) >> 23) & 0xff) - 126; }
+
+// What a value's size counts as for the reference: its scale, or its bias where
+// that is large (codes reach 15 scales).
+__device__ __forceinline__ float value_size(float scale, float bias) { return fmaxf(fabsf(scale), fabsf(bias) * 0.0625f); }
+
+// Whether a token's value scale and bias (as stored, bfloat16 bits) are in the
+// range of E; NaN and infinity are not.
+__device__ __forceinline__ bool in_range(uint32_t coef, int E)
+{
+    const uint32_t scale = (coef << 16) & 0x7fffffffu, bias = coef & 0x7fff0000u;
+    return (scale - (static_cast<uint32_t>(127 + E - kRange) << 23) < (static_cast<uint32_t>(kRange) << 23)) &
+           (bias < (static_cast<uint32_t>(127 + 4 + E) << 23));        // no branches
+}
 
 // The rows of one tile of query rows: request b, rows row0.. of its rows
 // (row = token * group + head), and the tokens [lo, hi) that any of them sees.
@@ -84,7 +120,7 @@ struct RowTile {
     int32_t q0;           // first query row of the request in the batch
     int32_t n_q, kv;      // its new tokens that have rows, and its tokens
     int32_t before;       // tokens before its first row's (below 0: that many rows see none)
-    int64_t row0, rows;
+    uint32_t row0, rows;  // below 2^31 (checked on the host)
     int32_t first, last;  // tokens of the tile's first and last row (below 0: before the request)
     int32_t lo, hi;
     bool poison;          // longer than the call allows
@@ -105,7 +141,7 @@ __device__ __forceinline__ int64_t tile_start(const AttnParams &p, int b)
     return int64_t(attn_cu(p, b)) * p.group / R + b;
 }
 
-__device__ __forceinline__ void tile_tokens(const AttnParams &p, RowTile &t, int64_t row0, int R)
+__device__ __forceinline__ void tile_tokens(const AttnParams &p, RowTile &t, uint32_t row0, int R)
 {
     t.kv = p.kv_len[t.b] < 0 ? 0 : p.kv_len[t.b];
     t.poison = t.kv > p.max_kv;
@@ -114,10 +150,11 @@ __device__ __forceinline__ void tile_tokens(const AttnParams &p, RowTile &t, int
     const int64_t before = int64_t(t.kv) - (int64_t(p.cu_q[t.b + 1]) - t.q0);
     t.before = static_cast<int32_t>(before < -INT32_MAX ? -INT32_MAX : before);
     t.row0 = row0;
-    t.rows = int64_t(t.n_q) * p.group;
-    const int64_t last = row0 + R < t.rows ? row0 + R : t.rows;
-    t.first = t.before + static_cast<int32_t>(row0 / p.group);
-    t.last = t.before + static_cast<int32_t>((last - 1) / p.group);
+    const uint32_t group = static_cast<uint32_t>(p.group);
+    t.rows = static_cast<uint32_t>(t.n_q) * group;
+    const uint32_t last = row0 + R < t.rows ? row0 + R : t.rows;
+    t.first = t.before + static_cast<int32_t>(row0 / group);
+    t.last = t.before + static_cast<int32_t>((last - 1) / group);
     t.hi = t.last < 0 ? 0 : t.last + 1;
     const int64_t lo = p.window > 0 ? int64_t(t.first) - p.window + 1 : 0;
     t.lo = lo < 0 ? 0 : lo < t.hi ? static_cast<int32_t>(lo) : t.hi;
@@ -141,7 +178,7 @@ __device__ __forceinline__ bool find_tile(const AttnParams &p, int64_t slot, Row
     // row starts that are not in order can make `b` a request that starts behind this slot
     const int64_t row0 = (slot - tile_start<R>(p, t.b)) * R;
     if (t.n_q <= 0 || row0 < 0 || row0 >= int64_t(t.n_q) * p.group) return false;
-    tile_tokens(p, t, row0, R);
+    tile_tokens(p, t, static_cast<uint32_t>(row0), R);
     return true;
 }
 
@@ -204,6 +241,15 @@ __device__ __forceinline__ f16x8 nibbles(uint32_t w, const NibbleBits &k)
 }
 constexpr int kOddCentre = 7;
 
+// Maximum (NaN ignored) over each run of 16 lanes.
+__device__ __forceinline__ float max_over_16(float v)
+{
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false)));
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false)));
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xF, 0xF, false)));
+    return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, false)));
+}
+
 // Maximum (NaN ignored) over the four lanes that share l % 16.
 __device__ __forceinline__ float max_over_groups(float v)
 {
@@ -233,9 +279,46 @@ __device__ __forceinline__ float attn_lse(const RowTile &t, float ref, float tot
            : total == 0.0f ? -__builtin_inff() : (ref + __log2f(total)) * 0.693147180559945309f;
 }
 
-template <bool MASKED>
-struct MaskTag {
-    static constexpr bool value = MASKED;
+// Exponents of the value sizes of a careful tile's tokens (up to 64), as a
+// reference follows them: of the smallest scale, and of the largest value less
+// kApart. Of one wave.
+struct alignas(16) TileSizes {
+    float low[64], top[64];
+};
+
+// Written a token a lane: `scales` and, `pitch` / 2 behind them, biases of NG
+// groups, `pitch` apart. Returns the size of the token's largest value.
+template <int NG>
+__device__ __forceinline__ float note_sizes(TileSizes &s, const float *scales, int pitch, int token)
+{
+    float low = __builtin_inff(), top = 0.0f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const float sc = scales[g * pitch + token] * (token & 1 ? 16.0f : 1.0f);
+        low = fminf(low, fabsf(sc));
+        top = fmaxf(top, value_size(sc, scales[g * pitch + pitch / 2 + token]));
+    }
+    int e = float_exponent(low);
+    e = e < kSmallest ? kSmallest : e > kLargest ? kLargest : e;
+    s.low[token] = static_cast<float>(e);
+    s.top[token] = static_cast<float>(float_exponent(top) - kApart);
+    return top;
+}
+
+// The range E for tokens of these sizes (one or more a lane).
+__device__ __forceinline__ int choose_range(float top)
+{
+    const int e = float_exponent(max_over_groups(max_over_16(top))) + kAbove;
+    return __builtin_amdgcn_readfirstlane(e < kSmallest ? kSmallest : e > kLargest ? kLargest : e);
+}
+
+template <bool CAREFUL>
+struct CareTag {
+    static constexpr bool value = CAREFUL;
+};
+template <int COUNT>
+struct Count {
+    static constexpr int value = COUNT;
 };
 
 // The query rows of a wave (QT tiles of 16, a row to the four lanes that share
@@ -247,20 +330,21 @@ struct QueryRows {
     static constexpr float kUnit = kTwo ? 1.0f : 5.9604644775390625e-08f;       // of a code as the matrix cores see it
     f16x8 qh[QT][NG][2], ql[kTwo ? QT : 1][NG][2];
     float qsum[QT][NG], factor[QT];
-    int32_t pos[QT];                                       // the row's token, -1 for no row or none
     f32x4 acc[QT][D / 16];
     float ref[QT], total[QT], bias[QT][NG];
 
-    __device__ __forceinline__ void load(const AttnParams &p, const RowTile &t, int kv_head, int64_t first, int lane)
+    // `pos` (LDS, 16 QT): the rows' tokens, -1 for no row or none; careful tiles
+    // read them there, the others have no register for them.
+    __device__ __forceinline__ void load(const AttnParams &p, const RowTile &t, int kv_head, uint32_t first, int lane, int32_t *pos)
     {
         const int col = lane & 15, g4 = lane >> 4;
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt) {
-            const int64_t row = first + qt * 16 + col;
+            const uint32_t row = first + qt * 16 + col;
             const bool live = row < t.rows;
-            const int32_t tok = live ? static_cast<int32_t>(row / p.group) : 0;
-            const int head = kv_head * p.group + (live ? static_cast<int>(row - int64_t(tok) * p.group) : 0);
-            pos[qt] = live ? max(t.before + tok, -1) : -1;
+            const uint32_t tok = live ? row / static_cast<uint32_t>(p.group) : 0;
+            const int head = kv_head * p.group + (live ? static_cast<int>(row - tok * p.group) : 0);
+            pos[qt * 16 + col] = live ? max(t.before + static_cast<int32_t>(tok), -1) : -1;
             const T *src = static_cast<const T *>(p.q) + int64_t(t.q0 + tok) * p.q_stride + int64_t(head) * D;
             float x[NG][2][8];
             float top = 0.0f;
@@ -333,35 +417,32 @@ struct QueryRows {
     }
 
     // Scores of NA blocks of 16 tokens into weights, the reference and the
-    // sums scaled where a score passes it. `base` is the first block's first
-    // token, vscale[g * pitch + token] the value scales (odd tokens: / 16),
-    // `top` the largest of them; visible: bit a * 4 + i.
-    template <bool MASKED, int NA>
-    __device__ __forceinline__ void weigh(const AttnParams &p, int qt, f32x4 (&x)[NA], uint32_t &visible, const float *vscale,
-                                          int pitch, float top, int32_t base, int g4)
+    // sums scaled where a score passes it. CAREFUL: `pos` is the row's token,
+    // `base` the first block's first token, `sizes` (from token `at` on) what
+    // note_sizes left, visible: bit a * 4 + i; else E is the range of the value scales.
+    template <bool CAREFUL, int NA>
+    __device__ __forceinline__ void weigh(const AttnParams &p, int qt, int32_t pos, f32x4 (&x)[NA], uint32_t &visible, const TileSizes *sizes,
+                                          int at, int E, int32_t base, int g4)
     {
-        float m = kNoReference, scale = top;
-        if constexpr (MASKED) {
+        float m = kNoReference, least = kNoReference, es = static_cast<float>(E);
+        if constexpr (CAREFUL) {
             visible = 0;
-            scale = 0.0f;
-            const int32_t last = pos[qt] - base;
+            es = static_cast<float>(kLargest);
+            const int32_t last = pos - base;
             const int32_t first = p.window > 0 ? last - p.window + 1 : -1;
 #pragma unroll
             for (int a = 0; a < NA; ++a) {
-                f32x4 sc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const f32x4 v = *reinterpret_cast<const f32x4 *>(vscale + g * pitch + a * 16 + g4 * 4);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[i] = fmaxf(sc[i], fabsf(v[i]) * (i & 1 ? 16.0f : 1.0f));
-                }
+                const f32x4 low = *reinterpret_cast<const f32x4 *>(&sizes->low[at + a * 16 + g4 * 4]);
+                const f32x4 top = *reinterpret_cast<const f32x4 *>(&sizes->top[at + a * 16 + g4 * 4]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int tok = a * 16 + g4 * 4 + i;
                     const bool see = tok <= last && tok >= first;
                     visible |= see ? 1u << (a * 4 + i) : 0u;
-                    m = see ? fmaxf(m, x[a][i] * factor[qt]) : m;
-                    scale = see ? fmaxf(scale, sc[i]) : scale;
+                    const float score = x[a][i] * factor[qt];
+                    m = fmaxf(m, see ? score : kNoReference);
+                    least = fmaxf(least, see ? score + top[i] : kNoReference);
+                    es = fminf(es, see ? low[i] : static_cast<float>(kLargest));
                 }
             }
         } else {
@@ -372,12 +453,7 @@ struct QueryRows {
                 for (int i = 0; i < 4; ++i) hi = fmaxf(hi, x[a][i]);
             m = fmaxf(m, hi * factor[qt]);
         }
-        // every value scale is below 2^es; the reference of a row is moved by
-        // what the row sees alone, so that nothing masked, and no other row,
-        // changes a bit of it
-        int es = static_cast<int>((__float_as_uint(scale) >> 23) & 0xff) - 126;
-        es = es < -60 ? -60 : es > 100 ? 100 : es;
-        const float want = m + (static_cast<float>(es) - kHead);
+        const float want = CAREFUL ? fmaxf(m + es, least) - kHead : m + (es - kHead);
         if (__any(want > ref[qt] + kSlack)) {
             const float most = max_over_groups(want);      // the four lanes of a row move together
             const float next = most > ref[qt] + kSlack ? most : ref[qt];
@@ -394,7 +470,7 @@ struct QueryRows {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float w = __builtin_amdgcn_exp2f(fmaf(x[a][i], factor[qt], -ref[qt]));
-                if constexpr (MASKED) w = visible >> (a * 4 + i) & 1u ? w : 0.0f;
+                if constexpr (CAREFUL) w = visible >> (a * 4 + i) & 1u ? w : 0.0f;
                 x[a][i] = w;
                 total[qt] += w;
             }
@@ -402,38 +478,73 @@ struct QueryRows {
 
     // Weights of 32 tokens (two blocks; value scales sc, biases bi of this
     // lane's) as the B operand of group g's output; their biases added up.
-    template <bool MASKED>
+    // CAREFUL: times a power of two that brings the row's largest product into
+    // [2^12, 2^13), and `down` its inverse.
+    template <bool CAREFUL>
     __device__ __forceinline__ void pieces(int qt, int g, f32x4 w0, f32x4 w1, uint32_t visible, const f32x4 (&sc)[2],
-                                           const f32x4 (&bi)[2], f16x8 &ph, f16x8 &pl)
+                                           const f32x4 (&bi)[2], f16x8 &ph, f16x8 &pl, float &down)
     {
+        const f32x4 s0 = sc[0], s1 = sc[1];
+        float up = 1.0f;
+        if constexpr (CAREFUL) {
+            // the products first: the power of two alone may leave what the weights can take
+            float top = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                // coefficients of tokens the row does not see may be anything
+                const bool see0 = visible >> r & 1u, see1 = visible >> (4 + r) & 1u;
+                bias[qt][g] = fmaf(w0[r], see0 ? bi[0][r] : 0.0f, bias[qt][g]);
+                bias[qt][g] = fmaf(w1[r], see1 ? bi[1][r] : 0.0f, bias[qt][g]);
+                w0[r] *= see0 ? s0[r] : 0.0f;
+                w1[r] *= see1 ? s1[r] : 0.0f;
+                top = fmaxf(top, fmaxf(fabsf(w0[r]), fabsf(w1[r])));
+            }
+            top = max_over_groups(top);
+            int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xff);
+            e = e < 13 ? 13 : e > 254 ? 254 : e;
+            up = __uint_as_float(static_cast<uint32_t>(127 + 12 + 127 - e) << 23);
+            down = __uint_as_float(static_cast<uint32_t>(127 - 12 - 127 + e) << 23);
+        }
         u32x4 hi, lo;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            float s0 = sc[0][r], s1 = sc[1][r], b0 = bi[0][r], b1 = bi[1][r];
-            if constexpr (MASKED) {
-                // coefficients of tokens the row does not see may be anything
-                const bool see0 = visible >> r & 1u, see1 = visible >> (4 + r) & 1u;
-                s0 = see0 ? s0 : 0.0f, b0 = see0 ? b0 : 0.0f;
-                s1 = see1 ? s1 : 0.0f, b1 = see1 ? b1 : 0.0f;
+            const float u0 = CAREFUL ? up : s0[r], u1 = CAREFUL ? up : s1[r];
+            if constexpr (!CAREFUL) {
+                bias[qt][g] = fmaf(w0[r], bi[0][r], bias[qt][g]);
+                bias[qt][g] = fmaf(w1[r], bi[1][r], bias[qt][g]);
             }
-            bias[qt][g] = fmaf(w0[r], b0, bias[qt][g]);
-            bias[qt][g] = fmaf(w1[r], b1, bias[qt][g]);
-            const uint32_t pair = pack_f16(w0[r] * s0, w1[r] * s1);
+            const uint32_t pair = pack_f16(w0[r] * u0, w1[r] * u1);
             hi[r] = pair;
             if constexpr (kTwo) {
                 const f16x2 hh = __builtin_bit_cast(f16x2, pair);
-                lo[r] = pack_f16(fmaf(w0[r], s0, -static_cast<float>(hh[0])), fmaf(w1[r], s1, -static_cast<float>(hh[1])));
+                lo[r] = pack_f16(fmaf(w0[r], u0, -static_cast<float>(hh[0])), fmaf(w1[r], u1, -static_cast<float>(hh[1])));
             }
         }
         ph = __builtin_bit_cast(f16x8, hi);
         if constexpr (kTwo) pl = __builtin_bit_cast(f16x8, lo);
     }
 
-    // Channels 16 db.. of the output: v the codes of 32 tokens.
-    __device__ __forceinline__ void add(int qt, int db, f16x8 v, f16x8 ph, f16x8 pl)
+    // 16 channels of output added to c: v the codes of 32 tokens.
+    __device__ __forceinline__ f32x4 product(f16x8 v, f16x8 ph, f16x8 pl, f32x4 c) const
     {
-        acc[qt][db] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, ph, acc[qt][db], 0, 0, 0);
-        if constexpr (kTwo) acc[qt][db] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pl, acc[qt][db], 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, ph, c, 0, 0, 0);
+        if constexpr (kTwo) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pl, c, 0, 0, 0);
+        return c;
+    }
+    // Channels 16 db.. of the output: N operands of 32 tokens each.
+    template <bool CAREFUL, int N>
+    __device__ __forceinline__ void add(int qt, int db, const f16x8 (&v)[N], const f16x8 *ph, const f16x8 *pl, float down)
+    {
+        if constexpr (CAREFUL) {
+            f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int n = 0; n < N; ++n) c = product(v[n], ph[n], pl[n], c);
+            acc[qt][db] = __builtin_elementwise_fma(c, f32x4{down, down, down, down}, acc[qt][db]);
+            asm("" : "+v"(acc[qt][db]));                   // kept as four registers in a row, as the matrix cores take them
+        } else {
+#pragma unroll
+            for (int n = 0; n < N; ++n) acc[qt][db] = product(v[n], ph[n], pl[n], acc[qt][db]);
+        }
     }
 
     // The lanes' sums joined, the biases added to the outputs.
@@ -455,15 +566,15 @@ struct QueryRows {
     }
 
     // Results of a split, or of the whole call.
-    __device__ __forceinline__ void write(const AttnParams &p, const RowTile &t, int kv_head, int64_t first, int lane) const
+    __device__ __forceinline__ void write(const AttnParams &p, const RowTile &t, int kv_head, uint32_t first, int lane) const
     {
         const int col = lane & 15, g4 = lane >> 4;
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt) {
-            const int64_t row = first + qt * 16 + col;
+            const uint32_t row = first + qt * 16 + col;
             if (row >= t.rows) continue;
-            const int32_t tok = static_cast<int32_t>(row / p.group);
-            const int head = kv_head * p.group + static_cast<int>(row - int64_t(tok) * p.group);
+            const uint32_t tok = row / static_cast<uint32_t>(p.group);
+            const int head = kv_head * p.group + static_cast<int>(row - tok * p.group);
             const int64_t orow = int64_t(t.q0 + tok) * p.q_heads + head;
             if (p.nsplit > 1) {
                 float *dst = p.part_out + (orow * p.nsplit + blockIdx.y) * D;
@@ -500,19 +611,9 @@ __device__ __forceinline__ bool all_visible(const AttnParams &p, const RowTile &
     return base + count - 1 <= t.first && (p.window <= 0 || base > t.last - p.window);
 }
 
-// Maximum of a non-negative value over each run of 16 lanes.
-__device__ __forceinline__ float max_over_16(float v)
-{
-    v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false)));
-    v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false)));
-    v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xF, 0xF, false)));
-    return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, false)));
-}
-
-// Coefficients of a token's groups (scale low, bias high), `known`: its page
-// is in the cache, `inside`: it is one of the request's tokens.
+// Coefficients of a token's groups (scale low, bias high).
 template <int NG>
-__device__ __forceinline__ void load_coefs(const uint8_t *src, bool known, bool inside, uint32_t (&c)[NG])
+__device__ __forceinline__ void load_coefs(const uint8_t *src, uint32_t (&c)[NG])
 {
     if constexpr (NG == 1) {
         c[0] = *reinterpret_cast<const uint32_t *>(src);
@@ -524,11 +625,15 @@ __device__ __forceinline__ void load_coefs(const uint8_t *src, bool known, bool 
 #pragma unroll
         for (int g = 0; g < NG; ++g) c[g] = v[g];
     }
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        if (!known) c[g] = 0x7fc07fc0u;      // a page outside the cache reads as NaN
-        if (!inside) c[g] = 0;               // places behind the last token hold anything
-    }
+}
+
+// What they count as (where they are used, so that no load is waited for before):
+// `known`: the token's page is in the cache, `inside`: it is one of the request's
+// tokens.
+__device__ __forceinline__ uint32_t coef_of(uint32_t c, bool known, bool inside)
+{
+    if (!known) c = 0x7fc07fc0u;             // a page outside the cache reads as NaN
+    return inside ? c : 0;                   // places behind the last token hold anything
 }
 
 typedef int i32x2 __attribute__((ext_vector_type(2)));

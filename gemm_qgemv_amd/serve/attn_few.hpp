@@ -5,7 +5,7 @@
 // groups that take tiles of tokens in turn. A tile's codes are fetched into
 // registers one tile ahead and passed through LDS; with RW = 1 a wave passes
 // its own tile to itself and waits for no other. The KW partial results meet
-// in LDS at the end.
+// in LDS at the end. Careful tiles (attn_common.hpp) go through 32 tokens at a time.
 //
 // 16 rows are the least a matrix instruction takes: with 4 query heads a
 // key/value head 12 columns are idle, and the vector work of a tile (600
@@ -46,17 +46,22 @@ struct TileLds {
     uint8_t codes[2 * kTok * kRow];                        // K, V
     // scale (V, odd tokens: / 16) and bias (float32 queries: + centre * scale) of K, V
     float co[2][D / 64][2][kTok];
-    float top[4];                                          // largest |value scale| of a staging wave
 };
 
-// Bytes of LDS a workgroup needs.
+// Bytes of LDS a workgroup needs for tiles (and for the join), and in all.
 template <int D>
-constexpr int few_lds_bytes()
+constexpr int few_tiles_bytes()
 {
     // RW = 1: a tile for each wave; RW = 2: two buffers for each pair of waves
     const int tiles = static_cast<int>(sizeof(TileLds<D, few_tile_tokens(D)>)) * 4;
     const int join = 4 * 16 * (D + 4) * 4;
     return tiles > join ? tiles : join;
+}
+template <int D>
+constexpr int few_lds_bytes()
+{
+    // and, for careful tiles, each wave's notes of a tile and its rows' tokens
+    return few_tiles_bytes<D>() + 4 * static_cast<int>(sizeof(TileSizes) + 16 * sizeof(int32_t));
 }
 
 // Three workgroups a compute unit (168 registers) up to 128 channels, two
@@ -67,7 +72,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 2 : 3) void attn_few_kerne
 {
     constexpr int KW = 4 / RW;                             // groups of waves that share out the tokens
     constexpr bool kTwo = sizeof(T) == 4;                  // float32: two pieces
-    constexpr int kTok = few_tile_tokens(D), NA = kTok / 16, NST = kTok / 32, NG = D / 64;
+    constexpr int kTok = few_tile_tokens(D), NG = D / 64;
     constexpr int R = 16 * RW;                             // query rows of the workgroup
     constexpr int kRow = D / 2, kSeg = kRow / 16;          // code bytes, 16-byte granules of a token
     extern __shared__ __align__(16) uint8_t lds[];
@@ -88,8 +93,10 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 2 : 3) void attn_few_kerne
     const int tiles = (end - begin + kTok - 1) / kTok;
 
     QueryRows<T, D, 1> rows;
-    const int64_t first_row = t.row0 + rw * 16;
-    rows.load(p, t, kv_head, first_row, lane);
+    const uint32_t first_row = t.row0 + rw * 16;
+    TileSizes &sizes = reinterpret_cast<TileSizes *>(lds + few_tiles_bytes<D>())[wave];
+    int32_t *const pos = reinterpret_cast<int32_t *>(lds + few_tiles_bytes<D>() + 4 * sizeof(TileSizes)) + wave * 16;
+    rows.load(p, t, kv_head, first_row, lane, pos);
 
     // ---- fetching tiles -----------------------------------------------------
     const int32_t *row_pages = p.table + int64_t(t.b) * p.table_stride;
@@ -113,14 +120,27 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 2 : 3) void attn_few_kerne
         page_ids = row_pages[(want < end ? want : end - 1) >> p.kv.page_shift];
     };
     u32x4 code[NBW][kPieces];
-    uint32_t coef[NBW][NG];                                 // lane: part (lane / 16) % 2, token lane % 16
-    auto fetch_tile = [&](int tile) {
+    uint32_t coef[NB][NG];                                  // lane: part (lane / 16) % 2, token lane % 16; of all blocks
+    int unknown = 0;                                        // bits: blocks whose page is outside the cache
+    auto fetch_tile = [&](int tile) __attribute__((always_inline)) {
         const int32_t base = begin + tile * kTok;
+        unknown = 0;
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+            const int32_t id = __builtin_amdgcn_readlane(page_ids, blk);
+            const bool known = static_cast<uint32_t>(id) < static_cast<uint32_t>(p.kv.num_pages);
+            const uint8_t *page = p.kv.data + (known ? id : 0) * p.kv.page_bytes + head_off;
+            const int at = (base + blk * 16) & page_mask;
+            load_coefs(page + ((D / 2) << p.kv.page_shift) + at * (D / 16) +
+                           static_cast<uint32_t>(((lane >> 4) & 1) * half + (lane & 15) * (D / 16)),
+                       coef[blk]);
+            unknown |= known ? 0 : 1 << blk;
+        }
 #pragma unroll
         for (int j = 0; j < NBW; ++j) {
             const int blk = rw + j * RW;
             const int32_t id = __builtin_amdgcn_readlane(page_ids, blk);
-            const bool known = id >= 0 && id < p.kv.num_pages;
+            const bool known = static_cast<uint32_t>(id) < static_cast<uint32_t>(p.kv.num_pages);
             const uint8_t *page = p.kv.data + (known ? id : 0) * p.kv.page_bytes + head_off;
             const int at = (base + blk * 16) & page_mask;
             const uint8_t *src = page + at * kRow;
@@ -132,14 +152,10 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 2 : 3) void attn_few_kerne
                     code[j][n] = *reinterpret_cast<const u32x4 *>(src + piece_part(n) * half + (n % (D / 128)) * 1024 +
                                                                   static_cast<uint32_t>(lane * 16));
             }
-            load_coefs(page + ((D / 2) << p.kv.page_shift) + at * (D / 16) +
-                           static_cast<uint32_t>(((lane >> 4) & 1) * half + (lane & 15) * (D / 16)),
-                       known, base + blk * 16 + (lane & 15) < end, coef[j]);
         }
     };
-    // the fetched tile into LDS; returns the largest |value scale| this wave saw
-    auto put_tile = [&](Tile &s) {
-        float top = 0.0f;
+    // the fetched tile into LDS (a plain one is known, and the request's, throughout)
+    auto put_tile = [&](Tile &s, int32_t base, auto care_tag) __attribute__((always_inline)) {
         const bool is_v = (lane >> 4) & 1;
         const float odd = is_v && (lane & 1) ? 0.0625f : 1.0f, centre = is_v && (lane & 1) ? kOddCentre : 8.0f;
 #pragma unroll
@@ -153,65 +169,76 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 2 : 3) void attn_few_kerne
             }
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const float sc = __uint_as_float(coef[j][g] << 16), bi = __uint_as_float(coef[j][g] & 0xffff0000u);
-                top = fmaxf(top, fabsf(sc));
+                uint32_t c = RW == 1 ? coef[j][g] : rw ? coef[j * RW + RW - 1][g] : coef[j * RW][g];
+                if constexpr (decltype(care_tag)::value) c = coef_of(c, (unknown >> blk & 1) == 0, base + blk * 16 + (lane & 15) < end);
+                const float sc = __uint_as_float(c << 16), bi = __uint_as_float(c & 0xffff0000u);
                 if (lane < 32) {
                     s.co[is_v][g][0][blk * 16 + (lane & 15)] = sc * odd;
                     s.co[is_v][g][1][blk * 16 + (lane & 15)] = kTwo ? fmaf(centre, sc, bi) : bi;
                 }
             }
         }
-        return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(max_over_16(top)), 16));    // the lanes of V
     };
 
+    int E = kAbove;                                         // range of plain tiles' value scales, up to 4 at first
     const NibbleBits bits;
-    // ---- one tile -------------------------------------------------------------
-    auto compute = [&](const Tile &s, float top, int32_t base, auto masked_tag) {
-        constexpr bool kMasked = decltype(masked_tag)::value;
+    // ---- TOKENS tokens of a tile, from block `first` on ---------------------
+    auto compute = [&](const Tile &s, int first, int32_t base, auto care_tag, auto tokens_tag) __attribute__((always_inline)) {
+        constexpr bool kCareful = decltype(care_tag)::value;
+        constexpr int kTokens = decltype(tokens_tag)::value, NA = kTokens / 16, NST = kTokens / 32;
         f32x4 x[NA];
 #pragma unroll
         for (int a = 0; a < NA; ++a) {
-            const int tok = a * 16 + col;
+            const int tok = (first + a) * 16 + col;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 const int seg = (g * 2 + (g4 >> 1)) ^ k_swizzle<D>(tok);
                 const u32x2 w = *reinterpret_cast<const u32x2 *>(s.codes + tok * kRow + seg * 16 + (g4 & 1) * 8);
                 rows.score(0, g, nibbles<kTwo>(w[0], bits), nibbles<kTwo>(w[1], bits),
-                           *reinterpret_cast<const f32x4 *>(&s.co[0][g][0][a * 16 + g4 * 4]),
-                           *reinterpret_cast<const f32x4 *>(&s.co[0][g][1][a * 16 + g4 * 4]), x[a]);
+                           *reinterpret_cast<const f32x4 *>(&s.co[0][g][0][(first + a) * 16 + g4 * 4]),
+                           *reinterpret_cast<const f32x4 *>(&s.co[0][g][1][(first + a) * 16 + g4 * 4]), x[a]);
             }
         }
         uint32_t visible = 0;
-        rows.template weigh<kMasked>(p, 0, x, visible, &s.co[1][0][0][0], 2 * kTok, top, base, g4);
+        rows.template weigh<kCareful>(p, 0, kCareful ? pos[col] : 0, x, visible, &sizes, first * 16, E, base + first * 16, g4);
         // out += V^T w: lane `col` of group g4 addresses the codes of token
         // 16 (col / 4) + 4 g4 + col % 4 and gets channel `col` of 16 tokens
         // (32-token tiles: of 8 tokens for each of two blocks of channels)
+        constexpr int kBlocks = kTok == 64 ? 1 : 2;          // blocks of 16 channels a read serves
+        const int v_tok = kTok == 64 ? (col >> 2) * 16 + g4 * 4 + (col & 3) : ((col >> 2) & 1) * 16 + g4 * 4 + (col & 3);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             __builtin_amdgcn_sched_barrier(0);               // or the operands of several groups are held at once
             f16x8 ph[NST], pl[NST];
+            float down = 1.0f;
 #pragma unroll
             for (int st = 0; st < NST; ++st) {
                 f32x4 sc[2], bi[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    sc[h] = *reinterpret_cast<const f32x4 *>(&s.co[1][g][0][(st * 2 + h) * 16 + g4 * 4]);
-                    bi[h] = *reinterpret_cast<const f32x4 *>(&s.co[1][g][1][(st * 2 + h) * 16 + g4 * 4]);
+                    sc[h] = *reinterpret_cast<const f32x4 *>(&s.co[1][g][0][(first + st * 2 + h) * 16 + g4 * 4]);
+                    bi[h] = *reinterpret_cast<const f32x4 *>(&s.co[1][g][1][(first + st * 2 + h) * 16 + g4 * 4]);
                 }
-                rows.template pieces<kMasked>(0, g, x[st * 2], x[st * 2 + 1], visible >> (st * 8), sc, bi, ph[st], pl[st]);
+                rows.template pieces<kCareful>(0, g, x[st * 2], x[st * 2 + 1], visible >> (st * 8), sc, bi, ph[st], pl[st], down);
             }
-            constexpr int kBlocks = kTok == 64 ? 1 : 2;      // blocks of 16 channels a read serves
-            const int tok = kTok == 64 ? (col >> 2) * 16 + g4 * 4 + (col & 3) : ((col >> 2) & 1) * 16 + g4 * 4 + (col & 3);
 #pragma unroll
             for (int n = 0; n < 4 / kBlocks; ++n) {
                 const int chunk = g * 4 + n * kBlocks + (kBlocks == 2 ? col >> 3 : 0);
-                const int seg = (chunk >> 1) ^ v_swizzle<D>(tok);
-                const i32x2 w = read_transposed(s.codes + (kTok + tok) * kRow + seg * 16 + (chunk & 1) * 8);
+                const int seg = (chunk >> 1) ^ v_swizzle<D>(v_tok);
+                const i32x2 w = read_transposed(s.codes + (kTok + v_tok) * kRow + seg * 16 + (chunk & 1) * 8);
+                auto operand = [&](int h) { return nibbles<kTwo, kOddCentre>(static_cast<uint32_t>(h ? w[1] : w[0]), bits); };
+                if constexpr (kBlocks == 2) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t codes = h ? static_cast<uint32_t>(w[1]) : static_cast<uint32_t>(w[0]);
-                    rows.add(0, kBlocks == 1 ? g * 4 + n : g * 4 + n * 2 + h, nibbles<kTwo, kOddCentre>(codes, bits), ph[kBlocks == 1 ? h : 0],
-                             pl[kBlocks == 1 ? h : 0]);
+                    for (int h = 0; h < 2; ++h) {
+                        const f16x8 v[1] = {operand(h)};
+                        rows.template add<kCareful>(0, g * 4 + n * 2 + h, v, ph, pl, down);
+                    }
+                } else if constexpr (kTokens == 64) {
+                    const f16x8 v[2] = {operand(0), operand(1)};
+                    rows.template add<kCareful>(0, g * 4 + n, v, ph, pl, down);
+                } else {
+                    const f16x8 v[1] = {operand(first / 2)};
+                    rows.template add<kCareful>(0, g * 4 + n, v, ph, pl, down);
                 }
             }
         }
@@ -223,42 +250,62 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 2 : 3) void attn_few_kerne
         fetch_tile(kw);
         if (kw + KW < tiles) fetch_pages(kw + KW);
     }
+    // whether round i's tile needs no care: every row sees all of its tokens, and
+    // the value scales (of the fetched tile; lanes of V) are in the range
     auto whole = [&](int i) {
         const int32_t base = begin + (kw + i * KW) * kTok;
         return base + kTok <= end && all_visible(p, t, base, kTok);
     };
-    auto advance = [&](int i, auto masked_tag) {
+    auto plain = [&](int i) {
+        if (unknown != 0 || !whole(i)) return false;
+        bool in = true;
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) in = in & in_range(coef[blk][g], E);
+        return (__ballot(in) >> 16 & 0xffff) == 0xffff;
+    };
+    auto advance = [&](int i, auto care_tag) __attribute__((always_inline)) {
         const int tile = kw + i * KW;
         const bool live = tile < tiles;
         asm volatile("" : "+v"(lane));
         col = lane & 15, g4 = lane >> 4;
         Tile &s = bufs[RW > 1 ? i & 1 : 0];
-        float top = 0.0f;
-        if (live) top = put_tile(s);
-        if constexpr (RW > 1) {
-            if (live && lane == 0) s.top[rw] = top;
-            __syncthreads();
-        } else {
-            wave_fence();
-        }
+        if (live) put_tile(s, begin + tile * kTok, care_tag);
+        if constexpr (RW > 1) __syncthreads();
+        else wave_fence();
         if (!live) return;
+        if constexpr (decltype(care_tag)::value) {
+            const float size = note_sizes<NG>(sizes, &s.co[1][0][0][0], 2 * kTok, lane % kTok);
+            wave_fence();
+            if (whole(i)) E = choose_range(size);            // alike in the waves that share the tile
+        }
         if (tile + KW < tiles) {
             fetch_tile(tile + KW);
             if (tile + 2 * KW < tiles) fetch_pages(tile + 2 * KW);
         }
-        if constexpr (RW > 1) {
+        if constexpr (decltype(care_tag)::value) {
+            // 32 tokens at a time, which need fewer registers
 #pragma unroll
-            for (int w = 0; w < RW; ++w) top = fmaxf(top, s.top[w]);
+            for (int first = 0; first < kTok / 16; first += 2) {
+                asm volatile("" : "+v"(lane));
+                col = lane & 15, g4 = lane >> 4;
+                compute(s, first, begin + tile * kTok, care_tag, Count<32>{});
+            }
+        } else {
+            compute(s, 0, begin + tile * kTok, care_tag, Count<kTok>{});
         }
-        compute(s, top, begin + tile * kTok, masked_tag);
         if constexpr (RW == 1) wave_fence();
     };
-    // a loop for tiles that need masks and one for those that do not (one loop
-    // with both in it moves the accumulators between two sets of registers);
-    // either has one barrier a round, so waves may be in different ones
-    for (int i = 0; i < trips;) {
-        for (; i < trips && !whole(i); ++i) advance(i, MaskTag<true>{});
-        for (; i < trips && whole(i); ++i) advance(i, MaskTag<false>{});
+    // plain tiles in a loop of their own (as one of two loops, or in one with the
+    // careful tiles, the accumulators are moved between sets of registers); either
+    // has one barrier a round, so waves may be in different ones
+    for (int i = 0; i < trips; ++i) {
+        while (plain(i)) {
+            advance(i, CareTag<false>{});
+            if (++i == trips) break;
+        }
+        if (i < trips) advance(i, CareTag<true>{});
     }
 
     // ---- the groups of waves joined --------------------------------------------
@@ -273,9 +320,11 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 2 : 3) void attn_few_kerne
     // the KW waves of a row group share its rows; 4 channels a thread
     const float *all = reinterpret_cast<const float *>(lds) + rw * KW * 16 * kPitch;
     constexpr int kQuads = D / 4;
+    uint32_t group = p.group;
+    asm volatile("" : "+s"(group));                        // or its reciprocal stays in a register from load() on
     for (int i = kw * 64 + lane; i < 16 * kQuads; i += KW * 64) {
         const int r = i / kQuads, d = (i % kQuads) * 4;
-        const int64_t row = first_row + r;
+        const uint32_t row = first_row + r;
         if (row >= t.rows) continue;
         float m = kNoReference, sum = 0.0f;
 #pragma unroll
@@ -291,8 +340,8 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 2 : 3) void attn_few_kerne
             sum = fmaf(f, src[D + 1], sum);
             o += f * *reinterpret_cast<const f32x4 *>(src + d);
         }
-        const int32_t tok = static_cast<int32_t>(row / p.group);
-        const int head = kv_head * p.group + static_cast<int>(row - int64_t(tok) * p.group);
+        const uint32_t tok = row / group;
+        const int head = kv_head * p.group + static_cast<int>(row - tok * group);
         const int64_t orow = int64_t(t.q0 + tok) * p.q_heads + head;
         if (p.nsplit > 1) {
             const int64_t at = orow * p.nsplit + blockIdx.y;

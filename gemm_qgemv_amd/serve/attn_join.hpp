@@ -43,7 +43,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p)
     t.q0 = attn_cu(p, t.b);
     t.n_q = attn_cu(p, t.b + 1) - t.q0;
     if (tok < t.q0 || tok - t.q0 >= t.n_q) return;
-    const int64_t r = (tok - t.q0) * p.group + head % p.group;
+    const uint32_t r = static_cast<uint32_t>(tok - t.q0) * p.group + head % p.group;
     tile_tokens(p, t, r / R * R, R);
     const int32_t from = t.lo / TOK * TOK;
     int n = static_cast<int>((int64_t(t.hi) - from + p.chunk - 1) / p.chunk);

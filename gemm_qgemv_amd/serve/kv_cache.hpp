@@ -17,8 +17,8 @@ namespace qg {
 
 struct KvView {
     uint8_t *data;
-    int64_t num_pages;
     int64_t page_bytes;    // of all heads
+    int32_t num_pages;
     int32_t block_bytes;   // of one head
     int32_t page_shift;    // log2(page_size)
     int32_t heads, dim;

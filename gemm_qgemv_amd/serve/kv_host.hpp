@@ -39,7 +39,7 @@ namespace {
 {
     qg::KvView v;
     v.data = static_cast<uint8_t *>(c.data);
-    v.num_pages = c.num_pages;
+    v.num_pages = static_cast<int32_t>(c.num_pages);
     v.block_bytes = static_cast<int32_t>(block_bytes(c));
     v.page_bytes = int64_t(c.kv_heads) * v.block_bytes;
     v.page_shift = __builtin_ctz(static_cast<unsigned>(c.page_size));

@@ -409,7 +409,10 @@ int qkv_read(int dtype, const qg_kv_cache *cache, const int32_t *slots, int64_t 
  * over the tokens j <= p, with window > 0 only those with j > p - window.
  * Codes enter the matrix cores exactly; float32 queries and weights as two
  * binary16 pieces (22 bits), bfloat16 queries exactly and their weights as
- * one; scales, softmax statistics and sums are float32. One token a request
+ * one; scales, softmax statistics and sums are float32. Every group of 64
+ * channels keeps these bits whatever the sizes of the others' values, where
+ * its weighted values are not 2^60 times smaller than another's of the head.
+ * Queries, and scales and biases of keys, are below 2^100 in size. One token a request
  * is a decode step, a few a speculation's check, many a prompt chunk: one
  * entry point, kernels chosen by the sizes. Results do not depend on the
  * schedule.

@@ -99,3 +99,130 @@ def test_plan_length_past_32_bits(torch):
     assert state_out.tolist() == [width, width] and pos.tolist() == [most, most + 1]
     assert table[1024:2048].tolist() == ring[:1024].tolist()
     assert table[2049:3073].tolist() == ring[1024:].tolist()
+
+
+# --- value scales far apart ----------------------------------------------------------
+
+def scale_values(c, exponents):
+    """Values of request b's token j, group g, times 2^exponents(b, j, g): the
+    stored bfloat16 scale and bias change by an exact power of two."""
+    G = c.D // 64
+    _, mid, _ = ref.parts(c.page, c.D, 1)
+    for b, kv in enumerate(c.kv_len):
+        for j in range(kv):
+            page, at = int(c.table[b, j // c.page]), j % c.page
+            for h in range(c.H):
+                co = np.ascontiguousarray(c.data[page, h, mid + at * G * 4:mid + (at + 1) * G * 4]).view("<u2")
+                x = ref.bf16_value(co).astype(np.float64) * np.repeat([2.0 ** exponents(b, j, g) for g in range(G)], 2)
+                c.data[page, h, mid + at * G * 4:mid + (at + 1) * G * 4] = ref.bf16_bits(x.astype(np.float32)).view(np.uint8)
+
+
+def constant_values(c, which, value):
+    """Values of the groups that which(b, j, g) names become `value`: scale 0."""
+    G = c.D // 64
+    _, mid, _ = ref.parts(c.page, c.D, 1)
+    for b, kv in enumerate(c.kv_len):
+        for j in range(kv):
+            page, at = int(c.table[b, j // c.page]), j % c.page
+            for g in range(G):
+                if which(b, j, g):
+                    o = mid + (at * G + g) * 4
+                    c.data[page, :, o:o + 4] = np.array([0, ref.bf16_bits(np.array([value], np.float32))[0]], "<u2").view(np.uint8)
+
+
+KINDS = ["few", "drafts", "rows", "prompt", "split"]
+
+
+def value_case(torch, dtype, kind, D, **kw):
+    H, G, lens = {"few": (2, 4, [(150, 1), (64, 1), (7, 1)]), "drafts": (1, 8, [(200, 3), (130, 4)]), "rows": (1, 6, [(170, 9), (90, 2)]),
+                  "prompt": (1, 4, [(220, 60)]), "split": (1, 4, [(1500, 2)])}[kind]
+    return AttnCase(torch, dtype, H, G, D, 16, lens, seed=3, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,apart", [(128, 10), (128, 20), (256, 14), (128, 40), (256, -30)])
+def test_attention_value_groups_of_other_sizes(torch, dtype, kind, D, apart):
+    """Every channel group keeps its bits, whatever the others' size (the bound
+    of a channel is made of its own values)."""
+    say("value groups", dtype, kind, D, apart)
+    c = value_case(torch, dtype, kind, D)
+    scale_values(c, lambda b, j, g: -apart if g & 1 else 0)
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,low,high,tame", [(64, 0, 12, 1.0), (64, -20, 20, 1.0), (128, -50, 50, 20.0), (256, 0, 30, 40.0)])
+def test_attention_value_tokens_of_other_sizes(torch, dtype, kind, D, low, high, tame):
+    """Tokens whose values differ by many binary orders, with weights that are
+    alike (large values decide) and that are not."""
+    say("value tokens", dtype, kind, D, low, high, tame)
+    rng = np.random.default_rng(9)
+    c = value_case(torch, dtype, kind, D, tame=tame)
+    e = rng.integers(low, high + 1, size=(c.B, int(c.kv_len.max()), D // 64))
+    scale_values(c, lambda b, j, g: int(e[b, j, g]))
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,size", [(64, 105), (128, 112), (64, 60), (128, -45), (256, -70), (64, -100)])
+def test_attention_values_of_any_size(torch, dtype, kind, D, size):
+    """Values that append stores and read-back returns as finite numbers."""
+    say("value size", dtype, kind, D, size)
+    c = value_case(torch, dtype, kind, D)
+    scale_values(c, lambda b, j, g: size)
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", KINDS)
+def test_attention_constant_value_groups(torch, dtype, kind):
+    """Groups of scale 0, everywhere, in some tokens, large and small ones;
+    and a large value among them that has next to no weight."""
+    say("constant values", dtype, kind)
+    for D, which, value in ((128, lambda b, j, g: g == 1, 0.0), (128, lambda b, j, g: True, 3.0), (64, lambda b, j, g: True, 2.0 ** 100),
+                            (256, lambda b, j, g: g == (j // 40) % 4, 1.0), (64, lambda b, j, g: j < 70, 0.0),
+                            (128, lambda b, j, g: j >= 70 and g == 0, 2.0 ** 60)):
+        c = value_case(torch, dtype, kind, D, tame=8.0)
+        constant_values(c, which, value)
+        c.check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("size", [30, 110])
+def test_attention_a_large_value_without_weight(torch, dtype, kind, size):
+    """One token of far larger values whose score is far below the others':
+    what it does not weigh it must not cost."""
+    say("weightless", dtype, kind, size)
+    c = value_case(torch, dtype, kind, 64)
+    for b, kv in enumerate(c.kv_len):
+        j = int(kv) // 3
+        slot = int(c.table[b, j // 16]) * 16 + j % 16
+        # its key, alike in all channels, is far from every query once these lean to one side
+        k = np.full((1, c.H * 64), -40.0, np.float32)
+        v = np.zeros((1, c.H * 64), np.float32)
+        v[0, ::2] = 1.0
+        ref.append(c.data, 16, c.H, 64, k, v, [slot])
+    c.q[:, :c.Hq * 64] += 2.0
+    scale_values(c, lambda b, j, g: size if j == int(c.kv_len[b]) // 3 else 0)
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("H,G,D,lens", [(1, 4, 128, [(900, 1), (640, 1)]), (1, 8, 64, [(800, 4)]), (1, 6, 256, [(700, 9)]), (1, 4, 64, [(800, 33)]),
+                                        (1, 4, 128, [(700, 40)])])
+@pytest.mark.parametrize("tame,window", [(1.0, 0), (25.0, 0), (4.0, 333)])
+def test_attention_values_that_change_size_along_a_request(torch, dtype, H, G, D, lens, tame, window):
+    """Runs of tokens whose values are alike, at sizes far apart, a few tokens
+    of other sizes among them: kernels go from one way of taking tiles to the
+    other and back."""
+    say("runs", dtype, D, lens, tame, window)
+    rng = np.random.default_rng(21)
+    c = AttnCase(torch, dtype, H, G, D, 16, lens, seed=5, tame=tame, window=window)
+    run = [0, -18, 14, 0, -33, 3, 40, -6]
+    odd = rng.integers(-30, 30, size=2000) * (rng.random(2000) < 0.004)
+    scale_values(c, lambda b, j, g: run[j // 131 % 8] + int(odd[j]) - 5 * (g & 1))
+    c.check()
