@@ -15,6 +15,10 @@ constexpr int64_t kAlign = 16;
 // Compute units of the MI355X.
 constexpr int64_t kComputeUnits = 256;
 
+// Workgroups of 256 threads in one dimension of a launch: it has fewer than 2^32
+// threads. (A larger grid is not reported as an error; part of it is not run.)
+constexpr int64_t kMaxWorkgroups = (int64_t(1) << 24) - 1;
+
 [[maybe_unused]] bool aligned(const void *p, int64_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 [[maybe_unused]] int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -36,7 +36,7 @@ __device__ __forceinline__ bool append_place(const AppendMap &m, int64_t n, int6
 }
 
 struct AppendParams {
-    const void *src[2];       // k, v
+    const char *src[2];       // k, v
     int64_t stride[2];        // elements between rows
     const int32_t *slots;
     int64_t n;
@@ -119,8 +119,8 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendParams 
     if (!append_place(p.map, p.n, t, c)) return;     // whole runs of 8 lanes leave together
     const int64_t slot = p.slots[t];
     float x[2][8];
-    load8(static_cast<const T *>(p.src[0]) + t * p.stride[0] + c, x[0]);
-    load8(static_cast<const T *>(p.src[1]) + t * p.stride[1] + c, x[1]);
+    load8(reinterpret_cast<const T *>(p.src[0]) + t * p.stride[0] + c, x[0]);
+    load8(reinterpret_cast<const T *>(p.src[1]) + t * p.stride[1] + c, x[1]);
     const int lane = threadIdx.x & 63;
     uint32_t codes[2], coef[2];
 #pragma unroll
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendParams 
 }
 
 struct ReadParams {
-    void *dst[2];
+    char *dst[2];
     int64_t stride[2];
     const int32_t *slots;
     int64_t n;
@@ -172,7 +172,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_read_kernel(ReadParams p)
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = fmaf(s, static_cast<float>((codes >> (4 * i)) & 15u), b);
     }
-    store8(static_cast<T *>(p.dst[part]) + t * p.stride[part] + c, x);
+    store8(reinterpret_cast<T *>(p.dst[part]) + t * p.stride[part] + c, x);
 }
 
 }  // namespace qg

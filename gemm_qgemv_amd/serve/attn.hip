@@ -92,7 +92,7 @@ int check_attn_sizes(const qg_kv_cache &c, int batch, int64_t total_q, int64_t m
         return QG_ERR_SHAPE;
     const AttnPlan a = plan_attn(c, batch, total_q, max_q, max_kv, q_heads);
     const int64_t rows = total_q * q_heads;
-    return a.slots * c.kv_heads > 0x7fffffffLL || rows > 0x7fffffffLL ? QG_ERR_SHAPE : QG_OK;
+    return a.slots * c.kv_heads > kMaxWorkgroups || rows > 0x7fffffffLL ? QG_ERR_SHAPE : QG_OK;
 }
 
 template <auto KERNEL>

@@ -23,16 +23,30 @@ Range rows_range(int dtype, const void *p, int64_t stride, int64_t width, int64_
     return range_of(p, ((n - 1) * stride + width) * (dtype == QG_F32 ? 4 : 2));
 }
 
-// `parts`: K and V in workgroups of their own (2) or together (1).
-qg::AppendMap append_map(const qg_kv_cache &c, int64_t n, unsigned parts, dim3 &grid)
+qg::AppendMap append_map(const qg_kv_cache &c)
 {
     qg::AppendMap m;
     m.per_row = c.kv_heads * c.head_dim / 8;
     m.rows = std::max(1, qg::kAppendThreads / m.per_row);
     m.inv = 1.0f / static_cast<float>(m.per_row);
-    grid = dim3(static_cast<unsigned>(ceil_div(n, m.rows)), parts,
-                static_cast<unsigned>(ceil_div(m.per_row, qg::kAppendThreads)));
     return m;
+}
+
+// Launches over all rows, in pieces that a grid holds. `parts`: K and V in
+// workgroups of their own (2) or together (1); side(p, i): K's and V's rows.
+template <typename P, typename Side>
+void launch_rows(void (*kernel)(P), P p, unsigned parts, int64_t element, Side side, hipStream_t stream)
+{
+    const int64_t n = p.n, most = kMaxWorkgroups * p.map.rows;
+    for (int64_t first = 0; first < n; first += most) {
+        p.n = std::min(n - first, most);
+        const dim3 grid(static_cast<unsigned>(ceil_div(p.n, p.map.rows)), parts,
+                        static_cast<unsigned>(ceil_div(p.map.per_row, qg::kAppendThreads)));
+        hipLaunchKernelGGL(kernel, grid, dim3(qg::kAppendThreads), 0, stream, p);
+        p.slots += p.n;
+        for (int i = 0; i < 2; ++i)
+            if (side(p, i)) side(p, i) += p.n * p.stride[i] * element;
+    }
 }
 
 }  // namespace
@@ -110,13 +124,11 @@ int qkv_append(int dtype, const void *k, int64_t k_stride, const void *v, int64_
     if ((st = check_alias(inputs, 3, written, 1)) != QG_OK) return st;
 
     (void)hipGetLastError();
-    dim3 grid;
-    const qg::AppendMap map = append_map(*cache, n, 1, grid);
-    qg::AppendParams p{{k, v}, {k_stride, v_stride}, slots, n, map, kv_view(*cache)};
-    if (dtype == QG_F32)
-        hipLaunchKernelGGL(qg::kv_append_kernel<float>, grid, dim3(qg::kAppendThreads), 0, stream, p);
-    else
-        hipLaunchKernelGGL(qg::kv_append_kernel<uint16_t>, grid, dim3(qg::kAppendThreads), 0, stream, p);
+    qg::AppendParams p{{static_cast<const char *>(k), static_cast<const char *>(v)}, {k_stride, v_stride}, slots, n,
+                       append_map(*cache), kv_view(*cache)};
+    auto src = [](qg::AppendParams &q, int i) -> const char *& { return q.src[i]; };
+    if (dtype == QG_F32) launch_rows(qg::kv_append_kernel<float>, p, 1, 4, src, stream);
+    else launch_rows(qg::kv_append_kernel<uint16_t>, p, 1, 2, src, stream);
     return launch_status();
 }
 
@@ -142,13 +154,10 @@ int qkv_read(int dtype, const qg_kv_cache *cache, const int32_t *slots, int64_t 
     if ((st = check_alias(inputs, 2, written, nw)) != QG_OK) return st;
 
     (void)hipGetLastError();
-    dim3 grid;
-    const qg::AppendMap map = append_map(*cache, n, 2, grid);
-    qg::ReadParams p{{k, v}, {k_stride, v_stride}, slots, n, map, kv_view(*cache)};
-    if (dtype == QG_F32)
-        hipLaunchKernelGGL(qg::kv_read_kernel<float>, grid, dim3(qg::kAppendThreads), 0, stream, p);
-    else
-        hipLaunchKernelGGL(qg::kv_read_kernel<uint16_t>, grid, dim3(qg::kAppendThreads), 0, stream, p);
+    qg::ReadParams p{{static_cast<char *>(k), static_cast<char *>(v)}, {k_stride, v_stride}, slots, n, append_map(*cache), kv_view(*cache)};
+    auto dst = [](qg::ReadParams &q, int i) -> char *& { return q.dst[i]; };
+    if (dtype == QG_F32) launch_rows(qg::kv_read_kernel<float>, p, 2, 4, dst, stream);
+    else launch_rows(qg::kv_read_kernel<uint16_t>, p, 2, 2, dst, stream);
     return launch_status();
 }
 

@@ -78,24 +78,28 @@ int qlogprobs(const float *logits, int64_t ld, int64_t rows, int64_t vocab, cons
 
     (void)hipGetLastError();
     qg::LogprobParams p{};
-    p.x = logits;
     p.ld = ld;
-    p.rows = rows;
     p.vocab = static_cast<int32_t>(vocab);
-    p.ids = ids;
     p.top = top;
-    p.logprob = logprob;
-    p.entropy = entropy;
-    p.rank = rank;
-    p.top_ids = top_ids;
-    p.top_logprobs = top_logprobs;
     p.nslice = a.nslice;
     p.slice = a.slice;
     if (a.nslice > 1) {
         p.part = static_cast<qg::f32x4 *>(ws);
         p.part_keys = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + stat_bytes(a, rows));
     }
-    hipLaunchKernelGGL(qg::logprob_kernel, dim3(static_cast<unsigned>(rows * a.nslice)), dim3(qg::kLpThreads), 0, stream, p);
+    // in pieces that a grid holds (rows are cut into slices only where they are few)
+    for (int64_t first = 0; first < rows; first += p.rows) {
+        p.rows = a.nslice > 1 ? rows : std::min(rows - first, kMaxWorkgroups);
+        p.x = logits + first * ld;
+        auto at = [&](auto *base, int64_t step) { return base ? base + first * step : nullptr; };
+        p.ids = at(ids, 1);
+        p.logprob = at(logprob, 1);
+        p.entropy = at(entropy, 1);
+        p.rank = at(rank, 1);
+        p.top_ids = at(top_ids, top);
+        p.top_logprobs = at(top_logprobs, top);
+        hipLaunchKernelGGL(qg::logprob_kernel, dim3(static_cast<unsigned>(p.rows * a.nslice)), dim3(qg::kLpThreads), 0, stream, p);
+    }
     if (a.nslice > 1)
         hipLaunchKernelGGL(qg::logprob_join_kernel, dim3(static_cast<unsigned>(rows)), dim3(qg::kLpJoinThreads), 0, stream, p);
     return launch_status();

@@ -433,8 +433,10 @@ int qkv_read(int dtype, const qg_kv_cache *cache, const int32_t *slots, int64_t 
  * least to the largest of them may hold anything. What masked places hold (codes or coefficients of tokens a row
  * does not see, NaN and infinities among them) does not matter.
  *   1 <= batch <= 65535, 1 <= total_q <= 2^31 - 1, 1 <= max_q, 1 <= max_kv
- *   <= 2^30, q_heads a multiple of kv_heads, q_heads <= 1024, scale finite
- *   and > 0, window >= 0, strides as in qkv_append.
+ *   <= 2^30, q_heads a multiple of kv_heads, q_heads <= 1024, total_q *
+ *   q_heads <= 2^31 - 1, batch * kv_heads + total_q * q_heads / 16 < 2^24
+ *   (a launch's workgroups), scale finite and > 0, window >= 0, strides as in
+ *   qkv_append.
  * Workspace: qkv_attn_workspace_bytes(...) for the same arguments (partial
  * sums where the keys of a request are split over workgroups).
  */

@@ -29,3 +29,15 @@ def test_only_tensors_and_addresses_are_taken_as_device_memory(host):
         q.qlogprobs(**dict(LP, logits=host), stream=0)
     with pytest.raises(TypeError):
         q.KVCache(host, 8, 16, 2, 64)
+
+
+def test_attention_launches_that_no_grid_holds():
+    """2^24 workgroups of 256 threads are more than a launch takes."""
+    from test_serve_abi_cpu import attn_err
+    c = cache(pages=4, heads=257)
+    most = (2 ** 24 - 1) // 257                     # requests; one workgroup a request and head
+    a = dict(cache=c, q_heads=257, q_stride=257 * 64, out_stride=257 * 64, total_q=1, max_q=1, max_kv=16)
+    assert attn_err(**a, batch=most + 1) == q.QG_ERR_SHAPE
+    assert q.qkv_attn_workspace_bytes(c, most + 1, 1, 1, 16, 257) == 0
+    # one fewer is looked at further
+    assert attn_err(**dict(a, out=at(1)), batch=most) == q.QG_ERR_ALIAS

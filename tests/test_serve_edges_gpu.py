@@ -226,3 +226,54 @@ def test_attention_values_that_change_size_along_a_request(torch, dtype, H, G, D
     odd = rng.integers(-30, 30, size=2000) * (rng.random(2000) < 0.004)
     scale_values(c, lambda b, j, g: run[j // 131 % 8] + int(odd[j]) - 5 * (g & 1))
     c.check()
+
+
+# --- more rows than one launch takes ---------------------------------------------------
+
+def test_logprobs_of_more_rows_than_a_launch(torch):
+    R = 2 ** 24 + 3
+    x = torch.zeros(R, 2, device="cuda")
+    x[:, 1] = torch.arange(R, device="cuda") % 7 - 3.0
+    ids = torch.ones(R, dtype=torch.int32, device="cuda")
+    lp, ent = torch.full((R + 8,), 77.0, device="cuda"), torch.empty(R, device="cuda")
+    rank, tid = torch.empty(R, dtype=torch.int32, device="cuda"), torch.empty(R, dtype=torch.int32, device="cuda")
+    tlp = torch.empty(R, device="cuda")
+    assert q.qlogprobs_workspace_bytes(R, 2, 1) == 0
+    q.qlogprobs(x, 2, R, 2, ids, 1, lp, ent, rank, tid, tlp)
+    torch.cuda.synchronize()
+    d = x[:, 1].double()
+    want = -torch.log1p(torch.exp(-d))
+    assert ((lp[:R].double() - want).abs() <= 2.0 ** -20 + 2.0 ** -22 * want.abs()).all() and (lp[R:] == 77).all()
+    assert torch.equal(rank, 1 + (d <= 0).int()) and torch.equal(tid, (d > 0).int())
+    assert ((tlp.double() + torch.log1p(torch.exp(-d.abs()))).abs() <= 2.0 ** -20).all()
+    p = torch.sigmoid(d)
+    assert ((ent.double() + p * want + (1 - p) * -torch.log1p(torch.exp(d))).abs() <= 2.0 ** -20).all()
+
+
+def test_append_and_read_of_more_tokens_than_a_launch(torch):
+    """A token of 17 heads of 64 channels is a workgroup's (36 GB of bfloat16
+    rows; nearly all slots lie outside the cache)."""
+    H, D, page, n = 17, 64, 16, 2 ** 24 + 5
+    W = H * D
+    at = [0, 2 ** 24 - 2, 2 ** 24 - 1, 2 ** 24, n - 1]
+    x = torch.empty(n, W, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for t in at:
+        x[t] = torch.randn(W, generator=g, device="cuda")
+    slots = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    slots[torch.tensor(at, device="cuda")] = torch.tensor([3, 17, 2, 31, 8], dtype=torch.int32, device="cuda")
+    data = Guarded(torch, 2 * H * ref.block_bytes(page, D), torch.uint8)
+    cache = q.KVCache(data.t, 2, page, H, D)
+    q.qkv_append(q.QG_BF16, x, W, x, W, slots, n, cache)
+    torch.cuda.synchronize()
+    rows = torch.stack([x[t] for t in at]).float().cpu().numpy()
+    want = np.full((2, H, ref.block_bytes(page, D)), 77, np.uint8)
+    ref.append(want, page, H, D, rows, rows, [3, 17, 2, 31, 8])
+    assert np.array_equal(data.numpy().reshape(want.shape), want)
+    x.fill_(1.0)
+    q.qkv_read(q.QG_BF16, cache, slots, n, None, 0, x, W)
+    torch.cuda.synchronize()
+    got = torch.stack([x[t] for t in at]).float().cpu().numpy()
+    w = torch.from_numpy(ref.read(want, page, H, D, [3, 17, 2, 31, 8], 1)).bfloat16().float().numpy()
+    assert np.array_equal(got, w)
+    assert torch.isnan(x[1:n - 1:4099]).all() and torch.isnan(x[n - 2]).all()
