@@ -177,15 +177,19 @@ int qkv_attn(int dtype, const void *q, int64_t q_stride, const qg_kv_cache *cach
         if (!ws || ws_bytes < need) return QG_ERR_WORKSPACE;
         if (!aligned(ws, kAlign)) return QG_ERR_ALIGN;
     }
-    const Range inputs[5] = {range_of(q, ((total_q - 1) * q_stride + width) * size),
-                             range_of(cache->data, cache_bytes(*cache)), range_of(block_table, batch * table_stride * 4),
+    const Rows q_rows{reinterpret_cast<uintptr_t>(q), total_q, q_stride * size, width * size};
+    const Rows out_rows{reinterpret_cast<uintptr_t>(out), total_q, out_stride * size, width * size};
+    if (overlap(q_rows, out_rows)) return QG_ERR_ALIAS;
+    const Range q_range = range_of(q, ((total_q - 1) * q_stride + width) * size);
+    const Range inputs[4] = {range_of(cache->data, cache_bytes(*cache)), range_of(block_table, batch * table_stride * 4),
                              range_of(cu_q, (int64_t(batch) + 1) * 4), range_of(kv_len, int64_t(batch) * 4)};
     Range written[3];
     int nw = 0;
     written[nw++] = range_of(out, ((total_q - 1) * out_stride + width) * size);
     if (lse) written[nw++] = range_of(lse, total_q * q_heads * 4);
     if (need > 0) written[nw++] = range_of(ws, static_cast<int64_t>(need));
-    if ((st = check_alias(inputs, 5, written, nw)) != QG_OK) return st;
+    if ((st = check_alias(inputs, 4, written, nw)) != QG_OK) return st;
+    if ((st = check_alias(&q_range, 1, written + 1, nw - 1)) != QG_OK) return st;      // out: by rows, above
 
     (void)hipGetLastError();
     qg::AttnParams p{};

@@ -18,6 +18,12 @@ int check_rows(int dtype, const void *p, int64_t stride, int64_t width)
     return aligned(p, kAlign) ? QG_OK : QG_ERR_ALIGN;
 }
 
+Rows rows_of(int dtype, const void *p, int64_t stride, int64_t width, int64_t n)
+{
+    const int64_t size = dtype == QG_F32 ? 4 : 2;
+    return Rows{reinterpret_cast<uintptr_t>(p), n, stride * size, width * size};
+}
+
 Range rows_range(int dtype, const void *p, int64_t stride, int64_t width, int64_t n)
 {
     return range_of(p, ((n - 1) * stride + width) * (dtype == QG_F32 ? 4 : 2));
@@ -147,11 +153,10 @@ int qkv_read(int dtype, const qg_kv_cache *cache, const int32_t *slots, int64_t 
     if (v && (st = check_rows(dtype, v, v_stride, width)) != QG_OK) return st;
     if (!aligned(slots, 4)) return QG_ERR_ALIGN;
     const Range inputs[2] = {range_of(cache->data, cache_bytes(*cache)), range_of(slots, n * 4)};
-    Range written[2];
-    int nw = 0;
-    if (k) written[nw++] = rows_range(dtype, k, k_stride, width, n);
-    if (v) written[nw++] = rows_range(dtype, v, v_stride, width, n);
-    if ((st = check_alias(inputs, 2, written, nw)) != QG_OK) return st;
+    for (const Range &w : {rows_range(dtype, k ? k : v, k ? k_stride : v_stride, width, n),
+                           rows_range(dtype, v ? v : k, v ? v_stride : k_stride, width, n)})
+        if ((st = check_alias(inputs, 2, &w, 1)) != QG_OK) return st;
+    if (k && v && overlap(rows_of(dtype, k, k_stride, width, n), rows_of(dtype, v, v_stride, width, n))) return QG_ERR_ALIAS;
 
     (void)hipGetLastError();
     qg::ReadParams p{{static_cast<char *>(k), static_cast<char *>(v)}, {k_stride, v_stride}, slots, n, append_map(*cache), kv_view(*cache)};

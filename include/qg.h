@@ -392,7 +392,8 @@ int qkv_append(int dtype, const void *k, int64_t k_stride, const void *v, int64_
  * qkv_read -- the values that n slots of the cache stand for.
  *   k, v   [n] rows as in qkv_append, of `dtype` (written): scale * code +
  *          bias in float32 (fused), rounded to nearest even for bfloat16.
- *          Either may be NULL.
+ *          Either may be NULL; both may be parts of the same wider rows
+ *          (one stride, no shared elements).
  *   slots  a slot outside the cache gives a row of quiet NaNs.
  */
 int qkv_read(int dtype, const qg_kv_cache *cache, const int32_t *slots, int64_t n, void *k,
@@ -417,7 +418,8 @@ int qkv_read(int dtype, const qg_kv_cache *cache, const int32_t *slots, int64_t 
  * entry point, kernels chosen by the sizes. Results do not depend on the
  * schedule.
  *   q, out   rows of q_heads * head_dim elements of `dtype`, q_stride and
- *            out_stride elements apart
+ *            out_stride elements apart; both may be parts of the same wider
+ *            rows (one stride, no shared elements)
  *   lse      float32 [total_q][q_heads], or NULL
  *   block_table  int32 [batch][table_stride]
  *   max_q    at least the longest request's rows (chooses the kernel; a

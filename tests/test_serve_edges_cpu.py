@@ -41,3 +41,17 @@ def test_attention_launches_that_no_grid_holds():
     assert q.qkv_attn_workspace_bytes(c, most + 1, 1, 1, 16, 257) == 0
     # one fewer is looked at further
     assert attn_err(**dict(a, out=at(1)), batch=most) == q.QG_ERR_ALIAS
+
+
+def test_rows_that_touch_each_other_are_refused():
+    """Rows of one wider buffer: side by side is accepted (see the GPU tests),
+    shared elements are not."""
+    from test_serve_abi_cpu import ATTN, err
+    c = cache()
+    rd = dict(dtype=q.QG_F32, cache=c, slots=at(3), n=4, k=at(1), k_stride=256, v=at(1) + 512, v_stride=256)
+    for kw in (dict(v=at(1) + 496), dict(v=at(1) + 528), dict(v=at(1) + 512, v_stride=260), dict(v=at(1)), dict(v=at(1) + 1024),
+               dict(v=at(1) - 496), dict(k_stride=128, v_stride=128)):
+        assert err(q.qkv_read, **dict(rd, **kw)) == q.QG_ERR_ALIAS, kw
+    at_once = dict(ATTN, cache=c, q=at(1), q_stride=512, out_stride=512)
+    for out in (at(1) + 1008, at(1) + 1040, at(1), at(1) + 2048):
+        assert err(q.qkv_attn, **dict(at_once, out=out)) == q.QG_ERR_ALIAS, out

@@ -7,6 +7,7 @@ import pytest
 
 import gemm_qgemv_amd as q
 import serve_ref as ref
+from gemm_qgemv_amd import tensors
 from test_serve_gpu import AttnCase, Guarded, dev, say
 
 pytestmark = pytest.mark.gpu
@@ -277,3 +278,49 @@ def test_append_and_read_of_more_tokens_than_a_launch(torch):
     w = torch.from_numpy(ref.read(want, page, H, D, [3, 17, 2, 31, 8], 1)).bfloat16().float().numpy()
     assert np.array_equal(got, w)
     assert torch.isnan(x[1:n - 1:4099]).all() and torch.isnan(x[n - 2]).all()
+
+
+# --- rows that are parts of wider ones ---------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,H,D,gap", [(1, 1, 64, 0), (37, 2, 128, 0), (50, 3, 64, 24), (9, 2, 256, 64)])
+def test_read_into_parts_of_one_buffer(torch, dtype, n, H, D, gap):
+    """Keys and values side by side in the rows of one buffer, as append takes
+    them; what lies between them stays."""
+    say("side by side", dtype, n, H, D, gap)
+    dt, td = (q.QG_F32, torch.float32) if dtype == "f32" else (q.QG_BF16, torch.bfloat16)
+    W, page = H * D, 16
+    wide = 2 * (W + gap)
+    rng = np.random.default_rng(6)
+    cache = tensors.kv_cache(n // page + 1, page, H, D)
+    cache.data.fill_(0xFF)
+    x = dev(torch, rng.standard_normal((n, wide)).astype(np.float32)).to(td)
+    slots = dev(torch, rng.permutation(cache.num_pages * page)[:n].astype(np.int32))
+    q.qkv_append(dt, x, wide, x[:, W + gap:], wide, slots, n, cache)
+    k, v = torch.empty(n, W, dtype=td, device="cuda"), torch.empty(n, W, dtype=td, device="cuda")
+    q.qkv_read(dt, cache, slots, n, k, W, v, W)
+    for first, second in ((0, W + gap), (W + gap, 0)):
+        buf = Guarded(torch, n * wide, td)
+        rows = buf.t.view(n, wide)
+        q.qkv_read(dt, cache, slots, n, rows[:, first:], wide, rows[:, second:], wide)
+        torch.cuda.synchronize()
+        got = buf.numpy().reshape(n, wide)
+        assert np.array_equal(got[:, first:first + W], k.float().cpu().numpy())
+        assert np.array_equal(got[:, second:second + W], v.float().cpu().numpy())
+        assert np.all(got[:, W:W + gap] == 77) and np.all(got[:, 2 * W + gap:] == 77)
+
+
+def test_attention_beside_its_queries(torch):
+    """Outputs in the same wider rows as the queries."""
+    c = AttnCase(torch, "f32", 2, 3, 64, 16, [(40, 7), (90, 2)])
+    want, want_lse = c.run()
+    W = c.Hq * c.D
+    both = torch.full((c.total, 2 * W + 8), 5.0, device="cuda")
+    both[:, :W] = c.q[:, :W]
+    lse = torch.empty(c.total, c.Hq, device="cuda")
+    q.qkv_attn(c.dt, both, 2 * W + 8, c.cache, dev(torch, c.table), c.width, dev(torch, c.cu), dev(torch, c.kv_len), c.B, c.total, 7,
+               c.max_kv, c.Hq, c.scale, 0, both[:, W + 4:], 2 * W + 8, lse)
+    torch.cuda.synchronize()
+    assert np.array_equal(both[:, W + 4:2 * W + 4].cpu().numpy().reshape(want.shape), want)
+    assert torch.equal(both[:, :W], c.q[:, :W]) and (both[:, W:W + 4] == 5).all() and (both[:, 2 * W + 4:] == 5).all()
+    assert np.array_equal(lse.cpu().numpy(), want_lse)
