@@ -52,6 +52,8 @@ class KVCache:
         self._struct = _KVCacheStruct(_ptr(data), self.num_pages, self.page_size, self.kv_heads, self.head_dim)
         self._ref = ctypes.byref(self._struct)
         need = lib().qkv_cache_bytes(self._ref)
+        if data is not None and not isinstance(data, int) and not data.is_contiguous():
+            raise ValueError("the cache's memory is not contiguous")
         if need and data is not None and not isinstance(data, int) and data.numel() * data.element_size() < need:
             raise ValueError(f"the cache's memory has {data.numel() * data.element_size()} bytes, its geometry needs {need}")
 

@@ -55,3 +55,17 @@ def test_rows_that_touch_each_other_are_refused():
     at_once = dict(ATTN, cache=c, q=at(1), q_stride=512, out_stride=512)
     for out in (at(1) + 1008, at(1) + 1040, at(1), at(1) + 2048):
         assert err(q.qkv_attn, **dict(at_once, out=out)) == q.QG_ERR_ALIAS, out
+
+
+def test_cache_memory_is_one_piece():
+    """A strided view has enough elements, but they do not lie where the
+    kernels look for them."""
+    import torch
+    n = q.qkv_cache_bytes(cache(data=None))
+    wide = torch.zeros(2 * n, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        q.KVCache(wide[::2], 8, 16, 2, 64)
+    with pytest.raises(ValueError):
+        q.KVCache(wide.view(2, n).t(), 8, 16, 2, 64)
+    assert q.KVCache(wide[n:], 8, 16, 2, 64).data.numel() == n
+    assert q.KVCache(wide.view(2, n), 8, 16, 2, 64).num_pages == 8
