@@ -415,8 +415,9 @@ int qkv_read(int dtype, const qg_kv_cache *cache, const int32_t *slots, int64_t 
  * its weighted values are not 2^60 times smaller than another's of the head.
  * Queries, and scales and biases of keys, are below 2^100 in size. One token a request
  * is a decode step, a few a speculation's check, many a prompt chunk: one
- * entry point, kernels chosen by the sizes. Results do not depend on the
- * schedule.
+ * entry point, kernels chosen by the sizes. Results repeat from call to call,
+ * on any stream; a row's rounding depends on the kernel, the splits and the
+ * rows it shares a tile with, hence on the sizes and on the batch around it.
  *   q, out   rows of q_heads * head_dim elements of `dtype`, q_stride and
  *            out_stride elements apart; both may be parts of the same wider
  *            rows (one stride, no shared elements)

@@ -324,3 +324,138 @@ def test_attention_beside_its_queries(torch):
     assert np.array_equal(both[:, W + 4:2 * W + 4].cpu().numpy().reshape(want.shape), want)
     assert torch.equal(both[:, :W], c.q[:, :W]) and (both[:, W:W + 4] == 5).all() and (both[:, 2 * W + 4:] == 5).all()
     assert np.array_equal(lse.cpu().numpy(), want_lse)
+
+
+# --- long contexts, windows in bfloat16, neighbours -----------------------------------------
+
+class LongCase:
+    """Requests of many tokens with random codes and coefficients, on the GPU;
+    sampled rows are compared with 64 bits there."""
+
+    def __init__(self, torch, dtype, H, G, D, page, lens, window=0, seed=0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.torch, self.H, self.G, self.D, self.page, self.window, self.lens = torch, H, G, D, page, window, lens
+        self.dt, self.td = (q.QG_F32, torch.float32) if dtype == "f32" else (q.QG_BF16, torch.bfloat16)
+        self.B, self.Hq = len(lens), H * G
+        self.width = -(-max(kv for kv, _ in lens) // page)
+        used = [-(-kv // page) for kv, _ in lens]
+        self.pages = sum(used) + 1
+        perm = torch.randperm(self.pages, generator=g, device="cuda").int()
+        self.table = torch.full((self.B, self.width), -1, dtype=torch.int32, device="cuda")
+        for b, n in enumerate(used):
+            self.table[b, :n] = perm[sum(used[:b]):sum(used[:b]) + n]
+        n_code, n_coef = page * D // 2, page * (D // 64) * 4
+        self.data = torch.empty(self.pages, H, ref.block_bytes(page, D), dtype=torch.uint8, device="cuda")
+        for part in range(2):
+            lo = part * (n_code + n_coef)
+            z = torch.randn(2, self.pages, H, n_code, generator=g, device="cuda").mul_(2.9).add_(7.5).round_().clamp_(0, 15).to(torch.uint8)
+            self.data[:, :, lo:lo + n_code] = z[0] | (z[1] << 4)
+            s = 0.15 + 0.3 * torch.rand(self.pages, H, n_coef // 4, generator=g, device="cuda")
+            b = -7.5 * s + 0.4 * torch.randn(self.pages, H, n_coef // 4, generator=g, device="cuda")
+            co = torch.stack([s, b], -1).bfloat16().view(torch.int16).reshape(self.pages, H, n_coef // 2).contiguous()
+            self.data[:, :, lo + n_code:lo + n_code + n_coef] = co.view(torch.uint8)
+        self.cu = np.concatenate([[0], np.cumsum([n for _, n in lens])]).astype(np.int32)
+        self.total, self.scale = int(self.cu[-1]), D ** -0.5
+        self.q = (torch.randn(self.total, self.Hq, D, generator=g, device="cuda") * 1.2).to(self.td)
+
+    def run(self):
+        torch = self.torch
+        cache = q.KVCache(self.data, self.pages, self.page, self.H, self.D)
+        max_q, max_kv = max(n for _, n in self.lens), max(kv for kv, _ in self.lens)
+        out, lse = torch.empty_like(self.q), torch.empty(self.total, self.Hq, device="cuda")
+        ws = tensors.attn_workspace(cache, self.B, self.total, max_q, max_kv, self.Hq)
+        kv_len = torch.tensor([kv for kv, _ in self.lens], dtype=torch.int32, device="cuda")
+        q.qkv_attn(self.dt, self.q, self.Hq * self.D, cache, self.table, self.width, dev(torch, self.cu), kv_len, self.B, self.total, max_q,
+                   max_kv, self.Hq, self.scale, self.window, out, self.Hq * self.D, lse, ws)
+        torch.cuda.synchronize()
+        return out, lse
+
+    def values(self, b, h, part, kv):
+        torch = self.torch
+        lo, mid, end = ref.parts(self.page, self.D, part)
+        blk = self.data[self.table[b, :-(-kv // self.page)].long(), h]
+        byte = blk[:, lo:mid]
+        code = torch.stack([byte & 15, byte >> 4], -1).double().reshape(-1, self.D // 64, 64)
+        co = blk[:, mid:end].contiguous().view(torch.bfloat16).double().reshape(-1, self.D // 64, 2)
+        size = (8 * co[..., :1].abs() + (co[..., 1:] + 8 * co[..., :1]).abs()).expand_as(code)
+        return (code * co[..., :1] + co[..., 1:]).reshape(-1, self.D)[:kv], size.reshape(-1, self.D)[:kv]
+
+    def check(self, got):
+        """Weights' rounding errors (2^-21 (1 + amp) each; bfloat16: 2^-12) and
+        those of the sums (kv / 32 additions, 2^-24 of the terms' sizes; 8 times
+        that for bfloat16's small codes) add up like random ones: six times
+        their root."""
+        torch = self.torch
+        out, lse = got
+        for b, (kv, n) in enumerate(self.lens):
+            for h in range(self.H):
+                k, kb = self.values(b, h, 0, kv)
+                v, vb = self.values(b, h, 1, kv)
+                for i in sorted({0, 1, n // 2, n - 1} & set(range(n))):
+                    p = kv - n + i
+                    lo = max(0, p - self.window + 1) if self.window else 0
+                    for j in sorted({h * self.G, (h + 1) * self.G - 1}):
+                        x = self.q[self.cu[b] + i, j].double()
+                        s = (k[lo:p + 1] @ x) * self.scale
+                        w = torch.softmax(s, 0)
+                        want, spread = w @ v[lo:p + 1], w @ vb[lo:p + 1]
+                        amp = float((kb[lo:p + 1] @ x.abs()).max()) * self.scale
+                        root = ((w * w) @ (vb[lo:p + 1] ** 2)).sqrt()
+                        tol = 6 * 2.0 ** -21 * (1 + amp) * root + 6 * 2.0 ** -24 * (p / 32 + 1) ** 0.5 * spread
+                        if self.dt == q.QG_BF16:
+                            tol = 8 * tol + 6 * 2.0 ** -12 * root + 2.0 ** -8 * want.abs()
+                        err = (out[self.cu[b] + i, j].double() - want).abs()
+                        assert (err <= tol).all(), (b, h, i, j, float((err / tol).max()))
+                        ref_lse = float(torch.logsumexp(s, 0))
+                        assert abs(float(lse[self.cu[b] + i, j]) - ref_lse) <= 2.0 ** -20 * (1 + amp) + 2.0 ** -22 * abs(ref_lse)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("H,G,D,page,lens,window", [
+    (2, 4, 128, 64, [(131071, 1)], 0), (2, 16, 64, 16, [(40001, 1), (9000, 1), (65536, 1)], 0), (1, 7, 256, 32, [(30000, 4), (20011, 5)], 0),
+    (1, 8, 64, 128, [(65537, 30)], 0), (8, 4, 128, 64, [(131072, 2048)], 0), (2, 4, 128, 16, [(50000, 1), (30000, 7)], 20011)])
+def test_attention_long_contexts(torch, dtype, H, G, D, page, lens, window):
+    """Up to 131072 tokens, in one piece (2048 rows) and in many; pages all over
+    a cache of up to 300 MB."""
+    say("long", dtype, H, G, D, lens, window)
+    c = LongCase(torch, dtype, H, G, D, page, lens, window)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("window", [1, 16, 65, 200])
+@pytest.mark.parametrize("H,G,D,page,lens", [(1, 4, 64, 16, [(701, 1), (3, 1), (130, 1)]), (2, 2, 128, 32, [(300, 5), (129, 2)]),
+                                             (1, 3, 128, 16, [(150, 150), (77, 20)]), (1, 2, 256, 64, [(333, 70)])])
+def test_attention_window_bf16(torch, window, H, G, D, page, lens):
+    say("window bf16", window, D, lens)
+    AttnCase(torch, "bf16", H, G, D, page, lens, window=window).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_alone_and_among_others(torch, dtype, D):
+    """A request's rows in a call of their own, and beside requests that bring
+    other tile heights and splits: each within the bound, so their difference
+    within twice that (their rounding may differ)."""
+    say("neighbours", dtype, D)
+    one = [(700, 2)]
+    alone = AttnCase(torch, dtype, 1, 4, D, 16, one, seed=7)
+    _, l, spread, amp = alone.want()
+    got = alone.run()
+    alone.check(got)
+    tol = spread * (2.0 ** -20 * (1 + amp[..., None]) + 2.0 ** -24 * (700 / 16 + 16))
+    if dtype == "bf16":
+        tol = tol + 2.0 ** -8 * np.abs(got[0]) + 2.0 ** -11 * spread
+    for others in ([(90, 3)], [(300, 90)], [(40, 1)] * 30):
+        c = AttnCase(torch, dtype, 1, 4, D, 16, one + others, seed=7)
+        # the same tokens and queries for the first request
+        for j in range(700):
+            a, b = (int(x.table[0, j // 16]) for x in (alone, c))
+            for part in range(2):
+                lo, mid, _ = ref.parts(16, D, part)
+                for at, size in ((lo, D // 2), (mid, D // 16)):
+                    at += j % 16 * size
+                    c.data[b, :, at:at + size] = alone.data[a, :, at:at + size]
+        c.q[:2] = alone.q
+        out, lse = c.run()
+        assert np.all(np.abs(out[:2] - got[0]) <= 2 * tol)
+        assert np.all(np.abs(lse[:2] - got[1]) <= 2 * (2.0 ** -20 * (1 + amp) + 2.0 ** -22 * np.abs(l)))
