@@ -6,6 +6,7 @@ Run ``python -m gemm_qgemv_amd.build``; ``__graft_entry__.build()`` calls
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
 import tempfile
@@ -32,6 +33,8 @@ FLAGS = [
     "-fno-gpu-flush-denormals-to-zero",
     # no packed-FP32 instructions (plain float code only)
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+    # what each kernel takes, for the check below
+    "-Rpass-analysis=kernel-resource-usage",
     "-I", os.path.join(ROOT, "include"),
 ]
 
@@ -58,12 +61,28 @@ def _hipcc(what: list[str], out: str, extra: list[str] | None, verbose: bool) ->
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError(f"hipcc failed to build {os.path.basename(out)}")
+    spills = spilling(res.stderr)
+    if spills:
+        raise RuntimeError(f"kernels of {' '.join(what)} keep registers in scratch memory: {', '.join(spills)}")
     errs = [l for l in res.stderr.splitlines()
             if "warning" in l and "packed-fp32-ops" not in l]
     if errs and verbose:
         sys.stderr.write("\n".join(errs) + "\n")
     os.replace(tmp, out)
     return out
+
+
+def spilling(remarks: str) -> list[str]:
+    """Names of the kernels that the compiler's resource remarks say spill
+    vector registers or use scratch memory: none may (a variant of the attention
+    kernels that spilled heavily was once seen to give wrong results, and a spill
+    in a loop over tiles costs more than what it makes room for)."""
+    names = []
+    for kernel in re.split(r"remark:\s+Function Name: ", remarks)[1:]:
+        numbers = re.findall(r"(?:VGPRs Spill|ScratchSize \[bytes/lane\]): (\d+)", kernel)
+        if any(int(n) for n in numbers):
+            names.append(kernel.split()[0])
+    return names
 
 
 if __name__ == "__main__":

@@ -69,3 +69,16 @@ def test_cache_memory_is_one_piece():
         q.KVCache(wide.view(2, n).t(), 8, 16, 2, 64)
     assert q.KVCache(wide[n:], 8, 16, 2, 64).data.numel() == n
     assert q.KVCache(wide.view(2, n), 8, 16, 2, 64).num_pages == 8
+
+
+def test_the_build_refuses_kernels_that_spill():
+    from gemm_qgemv_amd import build
+
+    def remarks(name, spilled, scratch):
+        at = f"serve/x.hpp:62:1: remark: "
+        return "".join(f"{at}{t} [-Rpass-analysis=kernel-resource-usage]\n" for t in (
+            f"Function Name: {name}", "    TotalSGPRs: 40", "    VGPRs: 168", f"    ScratchSize [bytes/lane]: {scratch}",
+            "    Occupancy [waves/SIMD]: 3", "    SGPRs Spill: 2", f"    VGPRs Spill: {spilled}"))
+    assert build.spilling(remarks("a", 0, 0) + remarks("b", 0, 0)) == []
+    assert build.spilling(remarks("a", 0, 0) + remarks("b", 1, 8) + remarks("c", 0, 16)) == ["b", "c"]
+    assert build.spilling("warning: something else\n") == []
