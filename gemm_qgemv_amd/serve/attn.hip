@@ -21,9 +21,9 @@ struct AttnPlan {
     int32_t chunk;
 
     // at most `most` splits of `tokens` tokens, of whole rounds. A few rounds
-    // stay in one split: the join would take longer (one row of 4 heads at 500
-    // tokens, 2 rounds: 10 us, 14 split; 16-row tiles at 3 rounds: 13.5 and 11.9;
-    // 40 rows at 130 tokens, 3 rounds: 16 us, 20 split, at 5 rounds 22 and 19)
+    // stay in one split: the join would take longer (one row of 4 heads of 128
+    // float32 channels: 2 rounds 10.9 us, 11.6 split, 3 rounds 13.8 and 12.3; 40
+    // rows: 3 rounds 12.5 and 12.1, 4 rounds 15.0 and 11.9)
     void split(int64_t tokens, int64_t most)
     {
         const int64_t rounds = (tokens + step - 1) / step;
@@ -49,8 +49,8 @@ AttnPlan plan_attn(const qg_kv_cache &c, int batch, int64_t total_q, int64_t max
     a.tile = few_or_rows_tile(c.head_dim, a.rows);
     a.step = a.tile * (a.rows == 16 ? 4 : a.rows == 32 ? 2 : 1);
     // two workgroups on every compute unit; four where decoding requests may
-    // differ in length (64 requests of 1024 to 8192 tokens: 117 us at two, 91
-    // at four, 94 at eight; one request of 131071: 47 at two, 53 at four)
+    // differ in length (64 requests of 1024 to 8192 tokens: 109 us at two, 90
+    // at four, 88 at eight; one request of 131071: 44.6 at two, 45.4 at four)
     const int64_t tiles = std::max<int64_t>(1, total_q * group / a.rows);
     const int64_t have = std::max(tiles, std::min<int64_t>(batch, total_q)) * c.kv_heads;
     const int64_t aim = (a.rows == 16 && batch > 1 ? 4 : 2) * kComputeUnits;
@@ -58,15 +58,14 @@ AttnPlan plan_attn(const qg_kv_cache &c, int batch, int64_t total_q, int64_t max
     // n splits take a workgroup rounds / n rounds, of 2 us or so, and n partial
     // results of every row written and read, at some terabytes a second: the
     // least sum is at a root (1280 rows of 128 float32 channels, 4000 tokens:
-    // 31 us in 32 splits, 39 in 63; 512 rows of 256, 12000 tokens: 30 us in 63
-    // splits, 39 in 188; decoding stays far below)
+    // 31 us in 21 splits, 32 in 32; decoding stays far below)
     const double rounds = static_cast<double>(ceil_div(max_kv, a.step));
     const double best = std::sqrt(rounds * 2e6 / (static_cast<double>(total_q) * q_heads * c.head_dim));
     const int64_t most_splits = std::min<int64_t>({want, std::llround(best), qg::kMaxSplits});
     // few splits of requests that may differ in length, half a round longer each:
     // the last ones, which start last, are then short and even out the end (64
-    // requests as above: 91 us, 98 with all alike; to 14000 tokens, 16 requests:
-    // 43 and 50)
+    // requests as above: 90 us, 93 with all alike; to 14000 tokens, 16 requests:
+    // 41 and 47)
     const bool even_out = a.rows <= 32 && batch > 1 && most_splits > 1 && most_splits <= 8;
     a.split(max_kv + (even_out ? most_splits * a.step / 2 : 0), most_splits);
     return a;
@@ -111,10 +110,10 @@ void launch_attn(const AttnPlan &a, const qg::AttnParams &p, hipStream_t s)
     if (a.nsplit == 1) return;
     constexpr int TOK = few_or_rows_tile(D, R);
     const int64_t rows = p.total_q * p.q_heads;
-    // a wave a row where splits are few or rows many (1280 rows, 32 splits: 19 us
-    // with attention, 27 with a workgroup a row; one row of 32 heads, 63 splits:
-    // a workgroup a row)
-    if (a.nsplit <= 16 || (a.nsplit <= 64 && rows >= 512))
+    // a wave a row where splits are few (64 ragged requests: 89.5 us, 91.5 with a
+    // workgroup a row; one row of 32 heads after 131071 tokens, 64 splits: 45.9, 44.8
+    // with a workgroup)
+    if (a.nsplit <= 16)
         hipLaunchKernelGGL((qg::attn_join_kernel<T, D, R, TOK, 1>), dim3(static_cast<unsigned>(ceil_div(rows, 4))), dim3(256), 0, s, p);
     else
         hipLaunchKernelGGL((qg::attn_join_kernel<T, D, R, TOK, 4>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, p);

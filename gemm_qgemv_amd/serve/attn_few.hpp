@@ -10,10 +10,11 @@
 // 16 rows are the least a matrix instruction takes: with 4 query heads a
 // key/value head 12 columns are idle, and the vector work of a tile (600
 // instructions of 64 tokens at 128 channels in float32, half of them to make
-// operands of the codes) is the same for 1 row as for 16. 64 bfloat16 requests
-// of 1024 to 8192 tokens (360 MB): 86 us, 4.2 TB/s, all of it from one page 70,
-// so half memory, half the waves' own chains; one float32 request of 131071
-// (151 MB): 45 us, 3.3 TB/s, from one page 39: the chains, at two waves a SIMD.
+// operands of the codes) is the same for 1 row as for 16. With the join: 64
+// bfloat16 requests of 1024 to 8192 tokens (360 MB) 90 us, 4.0 TB/s, all of it
+// from one page 71, so part memory, most the waves' own chains; one float32
+// request of 131071 (151 MB) 45 us, 3.4 TB/s, from one page 42: the chains, at two
+// waves a SIMD.
 #pragma once
 
 #include "attn_common.hpp"
@@ -65,8 +66,8 @@ constexpr int few_lds_bytes()
 }
 
 // Three workgroups a compute unit (168 registers) up to 128 channels, two
-// beyond: 64 requests of up to 8192 tokens, 128 channels, bfloat16: 105 us at
-// two, 91 at three.
+// beyond: 64 requests of up to 8192 tokens, 128 channels: float32 125 us at two,
+// 106 at three, bfloat16 89.6 and 89.5.
 template <typename T, int D, int RW>
 __global__ __launch_bounds__(kAttnThreads, D == 256 ? 2 : 3) void attn_few_kernel(AttnParams p)
 {

@@ -11,11 +11,11 @@
 // token its row is); V's go through a wave's own piece of LDS to be
 // transposed. Tiles are double buffered: one barrier a tile.
 //
-// 2048 float32 rows after 8192 tokens, 32 heads of 128 channels: 735 us (618
-// GFLOP in two pieces, 0.84 PFLOP/s; vector unit 57% and matrix cores 33% busy,
+// 2048 float32 rows after 8192 tokens, 32 heads of 128 channels: 737 us (618
+// GFLOP in two pieces, 0.84 PFLOP/s; vector unit 58% and matrix cores 33% busy,
 // seldom both). Six bfloat16 prompts of up to 4001 tokens, 32 heads of 64
-// channels: 541 us (vector unit 75%: a quarter-rate exponential and 8.5 other
-// instructions a score; matrix cores 18%).
+// channels: 514 us (vector unit 76%: a quarter-rate exponential and 8.5 other
+// instructions a score; matrix cores 20%).
 #pragma once
 
 #include "attn_common.hpp"
@@ -205,8 +205,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_rows_kernel(AttnParams p
             rows.template weigh<kCareful>(p, first + q, kCareful ? pos[(first + q) * 16 + (lane & 15)] : 0, x[q], visible[q],
                                           &sizes, 0, E, base, g4);
         // small groups of vector and matrix instructions in turn (2048 float32
-        // rows after 8192 cached tokens: 735 us, 750 without; with one product a
-        // piece, bfloat16, the compiler's own order is as good: 541 and 542)
+        // rows after 8192 cached tokens: 736 us, 751 without; with one product a
+        // piece, bfloat16, the compiler's own order is better, 513 and 549, and with
+        // 256 channels, 45.9 and 47.6)
         if constexpr (kTwo && D < 256) __builtin_amdgcn_iglp_opt(0);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
