@@ -15,10 +15,6 @@ constexpr int64_t kAlign = 16;
 // Compute units of the MI355X.
 constexpr int64_t kComputeUnits = 256;
 
-// Workgroups of 256 threads in one dimension of a launch: it has fewer than 2^32
-// threads. (A larger grid is not reported as an error; part of it is not run.)
-constexpr int64_t kMaxWorkgroups = (int64_t(1) << 24) - 1;
-
 [[maybe_unused]] bool aligned(const void *p, int64_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 [[maybe_unused]] int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -38,24 +34,6 @@ struct Range {
 [[maybe_unused]] bool overlap(Range a, Range b)
 {
     return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo;
-}
-
-// n rows of `width` bytes, `stride` bytes apart.
-struct Rows {
-    uintptr_t lo;
-    int64_t n, stride, width;
-};
-
-// Whether rows of two buffers share bytes. Rows as far apart in both may be parts
-// of the same wider rows; else a buffer counts from its first to its last byte.
-[[maybe_unused]] bool overlap(const Rows &a, const Rows &b)
-{
-    const auto end = [](const Rows &r) { return r.lo + static_cast<uintptr_t>((r.n - 1) * r.stride + r.width); };
-    if (!overlap(Range{a.lo, end(a)}, Range{b.lo, end(b)})) return false;
-    if (a.stride != b.stride) return true;
-    const bool up = b.lo >= a.lo;
-    const int64_t by = static_cast<int64_t>((up ? b.lo - a.lo : a.lo - b.lo) % static_cast<uintptr_t>(a.stride));
-    return by < (up ? a : b).width || by + (up ? b : a).width > a.stride;
 }
 
 // Every written range must be disjoint from every input range and from

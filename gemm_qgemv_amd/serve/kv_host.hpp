@@ -4,7 +4,7 @@
 
 #include <atomic>
 
-#include "../csrc/host_args.hpp"
+#include "host_rows.hpp"
 #include "kv_cache.hpp"
 
 namespace {

@@ -1,6 +1,6 @@
 // logprobs.hip -- entry point of the token log probabilities: checks, the
 // cut of rows into slices, launches.
-#include "../csrc/host_args.hpp"
+#include "host_rows.hpp"
 
 #include <algorithm>
 
