@@ -104,11 +104,12 @@ def test_plan_length_past_32_bits(torch):
 
 # --- value scales far apart ----------------------------------------------------------
 
-def scale_values(c, exponents):
-    """Values of request b's token j, group g, times 2^exponents(b, j, g): the
-    stored bfloat16 scale and bias change by an exact power of two."""
+def scale_values(c, exponents, part=1):
+    """Values (part 0: keys) of request b's token j, group g, times
+    2^exponents(b, j, g): the stored bfloat16 scale and bias change by an exact
+    power of two."""
     G = c.D // 64
-    _, mid, _ = ref.parts(c.page, c.D, 1)
+    _, mid, _ = ref.parts(c.page, c.D, part)
     for b, kv in enumerate(c.kv_len):
         for j in range(kv):
             page, at = int(c.table[b, j // c.page]), j % c.page
@@ -459,3 +460,15 @@ def test_attention_alone_and_among_others(torch, dtype, D):
         out, lse = c.run()
         assert np.all(np.abs(out[:2] - got[0]) <= 2 * tol)
         assert np.all(np.abs(lse[:2] - got[1]) <= 2 * (2.0 ** -20 * (1 + amp) + 2.0 ** -22 * np.abs(l)))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,by", [(64, 60), (128, -60), (128, 95), (64, -95), (256, 95)])
+def test_attention_keys_and_queries_of_any_size(torch, dtype, kind, D, by):
+    """Keys 2^by as large and queries 2^-by: the scores are as before."""
+    say("key size", dtype, kind, D, by)
+    c = value_case(torch, dtype, kind, D)
+    scale_values(c, lambda b, j, g: by, part=0)
+    c.q *= 2.0 ** -by
+    c.check()
