@@ -24,13 +24,20 @@ QG_WS_CONTROL_BYTES = 8192
 QG_F32, QG_BF16 = 1, 2
 QG_MAX_PLAN_BATCH = 8192
 QG_MAX_TOP = 64
+QMX_E2M1, QMX_E4M3 = 1, 2
+QMX_NONE, QMX_SILU_MUL = 0, 1
+QMX_MAX_K, QMX_MAX_M = 1 << 21, 1 << 24
+QMOE_MAX_EXPERTS, QMOE_MAX_TOP = 1024, 32
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqg.so")
 
 EXPORTS = ("qgemv", "qgemm", "qgemv_argmax", "qgemv_argmax_noalloc", "qembed",
            "qg_workspace_bytes", "qg_status_str", "qg_abi_version",
            "qkv_cache_bytes", "qkv_plan", "qkv_append", "qkv_read", "qkv_attn",
-           "qkv_attn_workspace_bytes", "qlogprobs", "qlogprobs_workspace_bytes")
+           "qkv_attn_workspace_bytes", "qlogprobs", "qlogprobs_workspace_bytes",
+           "qmx_scale_pitch", "qmx_quant", "qmx_dequant", "qmx_gemm", "qmx_gemm_workspace_bytes",
+           "qmoe_plan", "qmoe_plan_workspace_bytes", "qmoe_route", "qmoe_gemm", "qmoe_gemm_workspace_bytes",
+           "qmoe_combine")
 
 _lib = None
 
@@ -94,6 +101,22 @@ def lib() -> ctypes.CDLL:
         L.qkv_attn_workspace_bytes.argtypes = [P, I32, I64, I64, I64, I32]
         L.qlogprobs.argtypes = [P, I64, I64, I64, P, I32, P, P, P, P, P, P, SZ, P]
         L.qlogprobs_workspace_bytes.argtypes = [I64, I64, I32]
+        L.qmx_scale_pitch.argtypes = [I64]
+        L.qmx_scale_pitch.restype = I64
+        L.qmx_quant.argtypes = [I32, P, I64, I64, I64, I32, P, P, P]
+        L.qmx_dequant.argtypes = [I32, P, P, I64, I64, I32, P, I64, P]
+        L.qmx_gemm.argtypes = [I32, P, P, P, P, I32, I32, P, I64, I64, I64, P, SZ, P]
+        L.qmx_gemm_workspace_bytes.argtypes = [I32, I32, I64, I64, I64]
+        L.qmoe_plan.argtypes = [P, I64, I32, I32, P, P, P, P, SZ, P]
+        L.qmoe_plan_workspace_bytes.argtypes = [I64, I32, I32]
+        L.qmoe_route.argtypes = [I32, P, I64, I64, I32, I32, I32, P, P, P, P, P, P, SZ, P]
+        L.qmoe_gemm.argtypes = [I32, P, P, P, P, P, P, I64, I32, I32, I32, I32, P, I64, I64, P, SZ, P]
+        L.qmoe_gemm_workspace_bytes.argtypes = [I32, I32, I64, I32, I32, I64, I64]
+        L.qmoe_combine.argtypes = [I32, P, P, P, I64, I32, I64, I32, P, P]
+        for f in (L.qmx_gemm_workspace_bytes, L.qmoe_plan_workspace_bytes, L.qmoe_gemm_workspace_bytes):
+            f.restype = SZ
+        for f in (L.qmx_quant, L.qmx_dequant, L.qmx_gemm, L.qmoe_plan, L.qmoe_route, L.qmoe_gemm, L.qmoe_combine):
+            f.restype = I32
         for f in (L.qkv_cache_bytes, L.qkv_attn_workspace_bytes, L.qlogprobs_workspace_bytes):
             f.restype = SZ
         for f in (L.qgemv, L.qgemm, L.qgemv_argmax, L.qgemv_argmax_noalloc, L.qembed,
@@ -221,6 +244,60 @@ def qlogprobs(logits, ld, rows, vocab, ids, top, logprob, entropy, rank, top_ids
 
 def qlogprobs_workspace_bytes(rows, vocab, top) -> int:
     return int(lib().qlogprobs_workspace_bytes(rows, vocab, top))
+
+
+def qmx_scale_pitch(K) -> int:
+    return int(lib().qmx_scale_pitch(K))
+
+
+def qmx_quant(dtype, x, x_stride, rows, K, fmt, codes, scales, stream=None):
+    _check(lib().qmx_quant(dtype, _ptr(x), x_stride, rows, K, fmt, _ptr(codes), _ptr(scales), _stream(stream)), "qmx_quant")
+
+
+def qmx_dequant(fmt, codes, scales, rows, K, dtype, x, x_stride, stream=None):
+    _check(lib().qmx_dequant(fmt, _ptr(codes), _ptr(scales), rows, K, dtype, _ptr(x), x_stride, _stream(stream)),
+           "qmx_dequant")
+
+
+def qmx_gemm(xfmt, x_codes, x_scales, w_codes, w_scales, act, dtype, y, M, K, N, ws=None, ws_bytes=None, stream=None):
+    _check(lib().qmx_gemm(xfmt, _ptr(x_codes), _ptr(x_scales), _ptr(w_codes), _ptr(w_scales), act, dtype, _ptr(y),
+                          M, K, N, _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream)), "qmx_gemm")
+
+
+def qmx_gemm_workspace_bytes(xfmt, act, M, K, N) -> int:
+    return int(lib().qmx_gemm_workspace_bytes(xfmt, act, M, K, N))
+
+
+def qmoe_plan(ids, rows, experts, top, offsets, order, slots, ws=None, ws_bytes=None, stream=None):
+    _check(lib().qmoe_plan(_ptr(ids), rows, experts, top, _ptr(offsets), _ptr(order), _ptr(slots), _ptr(ws),
+                           _nbytes(ws, ws_bytes), _stream(stream)), "qmoe_plan")
+
+
+def qmoe_plan_workspace_bytes(rows, experts, top) -> int:
+    return int(lib().qmoe_plan_workspace_bytes(rows, experts, top))
+
+
+def qmoe_route(dtype, logits, ld, rows, experts, top, renorm, ids, weights, offsets, order, slots, ws=None,
+               ws_bytes=None, stream=None):
+    _check(lib().qmoe_route(dtype, _ptr(logits), ld, rows, experts, top, renorm, _ptr(ids), _ptr(weights),
+                            _ptr(offsets), _ptr(order), _ptr(slots), _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream)),
+           "qmoe_route")
+
+
+def qmoe_gemm(xfmt, x_codes, x_scales, w_codes, w_scales, offsets, order, rows, experts, top, act, dtype, y, M, K,
+              ws=None, ws_bytes=None, stream=None):
+    _check(lib().qmoe_gemm(xfmt, _ptr(x_codes), _ptr(x_scales), _ptr(w_codes), _ptr(w_scales), _ptr(offsets),
+                           _ptr(order), rows, experts, top, act, dtype, _ptr(y), M, K, _ptr(ws),
+                           _nbytes(ws, ws_bytes), _stream(stream)), "qmoe_gemm")
+
+
+def qmoe_gemm_workspace_bytes(xfmt, act, rows, experts, top, M, K) -> int:
+    return int(lib().qmoe_gemm_workspace_bytes(xfmt, act, rows, experts, top, M, K))
+
+
+def qmoe_combine(dtype, y, slots, weights, rows, top, M, out_dtype, out, stream=None):
+    _check(lib().qmoe_combine(dtype, _ptr(y), _ptr(slots), _ptr(weights), rows, top, M, out_dtype, _ptr(out),
+                              _stream(stream)), "qmoe_combine")
 
 
 def qg_workspace_bytes(op, fmt, M, K, rows) -> int:

@@ -14,9 +14,11 @@ from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-# the low-bit products, and the serving-step operators
+# the low-bit products, the serving-step operators, microscaled numbers and experts
 SOURCES = [os.path.join(HERE, "csrc", "qg.hip"), os.path.join(HERE, "serve", "kv.hip"),
-           os.path.join(HERE, "serve", "attn.hip"), os.path.join(HERE, "serve", "logprobs.hip")]
+           os.path.join(HERE, "serve", "attn.hip"), os.path.join(HERE, "serve", "logprobs.hip"),
+           os.path.join(HERE, "mx", "quant.hip"), os.path.join(HERE, "mx", "mx_gemm.hip"),
+           os.path.join(HERE, "mx", "moe.hip")]
 OUT = os.path.join(HERE, "libqg.so")
 PROBE_SRC = os.path.join(HERE, "csrc", "probe.hip")
 PROBE_OUT = os.path.join(HERE, "libqgprobe.so")

@@ -1,0 +1,155 @@
+// mx_gemm.hpp -- products of MX activations with e2m1 weights on the scaled
+// matrix instructions of gfx950: what the kernel for few rows and the tiled
+// one share.
+//
+//   y[n][m] = sum over k of x[n][k] * w[m][k],      or with SILU, W holding 2 M
+//   rows, g from rows 0..M-1 and u from rows M..2M-1:  y = g / (1 + exp(-g)) * u
+//
+// The codes and the scale bytes go to the matrix cores as they lie in memory:
+// every instruction takes one scale a lane and block of 32 inputs, multiplies
+// exactly and adds in float32.
+//
+// Operand layout (measured against a 64-bit product; lane l of 64, R = 16 or 32 rows,
+// r = l % R, g = l / R; an instruction takes 64 / R blocks of 32 inputs):
+//   e2m1   row r, inputs 32 g .. 32 g + 31 (16 bytes)
+//   e4m3   row r, bytes 0..15 inputs 16 g .., bytes 16..31 inputs 1024 / R + 16 g ..
+//   scale  one byte: that of row r's block g
+//   D      column r; R = 16: rows 4 g .. 4 g + 3; R = 32: rows 8 i + 4 g .. + 3, i = 0..3
+//
+// Precision. Within an instruction the products of 8 neighbouring inputs are
+// aligned to the largest of them (to the sum of its factors' exponents, E) and
+// what lies below 2^(E - 13) is dropped; sums of these and across blocks keep
+// float32's 24 bits (measured: one product beside another, at every distance and
+// ratio). Products of two e2m1 numbers are multiples of 2^-2 with E <= 4: always
+// whole. e4m3 numbers reach from 2^-9 to 448, so they are taken in two parts, |x|
+// >= 4 (products with e2m1: multiples of 2^-2, E <= 10) and the rest (multiples of
+// 2^-10, E <= 3), each of which is whole in an instruction of its own. One
+// instruction for both would halve the work, with errors up to 2^-11 of sum |x w|.
+//
+// Grouped form (an experts' layer): rows are sorted by expert, offsets[e] is
+// expert e's first, and every tile of rows is one expert's.
+#pragma once
+
+#include "mx_common.hpp"
+
+namespace qg {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+struct MxGemmParams {
+    const uint8_t *xc, *xs, *wc, *ws;
+    void *y;
+    int64_t M;               // outputs a row
+    int64_t N;               // rows (grouped: pairs)
+    int32_t K, pitch;        // inputs a row, bytes of a row of scales
+    int32_t tiles_m, tiles_n;
+    bool vec;                // M is a multiple of 4
+    // grouped only
+    const int32_t *offsets;  // [experts + 1]
+    const int32_t *order;    // pair of each sorted row, or NULL: x lies sorted
+    int32_t experts;
+    int64_t x_rows;          // rows of x where `order` is given
+    FastDiv top;
+};
+
+// Four e4m3 numbers as those of at least 4 in size (NaN too) and the others,
+// zeros in the others' places: 4 is code 0x48.
+__device__ __forceinline__ void e4m3_parts(uint32_t x, int &large, int &small)
+{
+    const uint32_t top = ((x & 0x7f7f7f7fu) + 0x38383838u) & 0x80808080u;
+    const uint32_t mask = top | (top - (top >> 7));
+    large = static_cast<int>(x & mask);
+    small = static_cast<int>(x & ~mask);
+}
+
+// Operands of x: one of e2m1, two parts of e4m3.
+template <int XF> constexpr int kXParts = XF == kMxE2M1 ? 1 : 2;
+
+template <int XF>
+__device__ __forceinline__ void x_operands(u32x4 lo, u32x4 hi, i32x8 (&b)[kXParts<XF>])
+{
+    if constexpr (XF == kMxE2M1) {
+        b[0] = i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), 0, 0, 0, 0};
+    } else {
+        int l[8], s[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            e4m3_parts(lo[i], l[i], s[i]);
+            e4m3_parts(hi[i], l[4 + i], s[4 + i]);
+        }
+        b[0] = i32x8{l[0], l[1], l[2], l[3], l[4], l[5], l[6], l[7]};
+        b[1] = i32x8{s[0], s[1], s[2], s[3], s[4], s[5], s[6], s[7]};
+    }
+}
+
+// One expert's rows r0..r1-1 (at most T): the item-th such tile of all, expert
+// by expert; e = -1 if there are fewer. Every wave finds it by itself from one
+// round of loads (a lane takes ceil(experts / 64) experts side by side).
+// Offsets out of range are cut, so that any contents give rows in [0, pairs).
+struct GroupTile {
+    int e, r0, r1;
+};
+
+constexpr int kMaxExperts = 1024;
+
+template <int T>
+__device__ __forceinline__ GroupTile group_tile(const int32_t *offsets, int experts, int64_t pairs, int item)
+{
+    constexpr int C = kMaxExperts / 64;
+    const int lane = threadIdx.x & 63, c = (experts + 63) >> 6, first = lane * c;
+    int o[C + 1];
+#pragma unroll
+    for (int j = 0; j <= C; ++j)
+        if (j <= c) o[j] = offsets[min(first + j, experts)];
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j <= C; ++j)
+        if (j <= c) {
+            o[j] = static_cast<int>(max(int64_t(0), min(int64_t(o[j]), pairs)));
+            if (j > 0) mine += (max(o[j] - o[j - 1], 0) + (T - 1)) / T;
+        }
+    const int upto = wave_inclusive_sum32(mine);
+    const uint64_t after = __ballot(upto > item);
+    if (after == 0) return GroupTile{-1, 0, 0};
+    int rest = item - (upto - mine);
+    GroupTile t{0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+        if (j < c) {
+            const int n = max(o[j + 1] - o[j], 0), tiles = (n + (T - 1)) / T;
+            if (rest >= 0 && rest < tiles) {
+                t.e = first + j;
+                t.r0 = o[j] + rest * T;
+                t.r1 = min(t.r0 + T, o[j] + n);
+            }
+            rest -= tiles;
+        }
+    const int owner = __builtin_ctzll(after);
+    t.e = __builtin_amdgcn_readlane(t.e, owner);
+    t.r0 = __builtin_amdgcn_readlane(t.r0, owner);
+    t.r1 = __builtin_amdgcn_readlane(t.r1, owner);
+    return t;
+}
+
+// Row `at` of a tile's `rows`, as an index of rows of x behind the tile's first
+// (behind x's first where `order` is given); -1: none, it reads as zeros.
+template <bool GROUPED>
+__device__ __forceinline__ int64_t x_row(const MxGemmParams &p, int64_t r0, int rows, int at)
+{
+    if (at >= rows) return -1;
+    if (!GROUPED || !p.order) return at;
+    const int64_t pair = p.order[r0 + at];
+    if (pair < 0 || pair >= p.N) return -1;
+    const int64_t row = static_cast<uint32_t>(pair) / p.top;
+    return row < p.x_rows ? row : -1;
+}
+
+// g / (1 + exp(-g)) * u, with the exponential of a negative number only (it does not overflow).
+__device__ __forceinline__ float silu_mul(float g, float u)
+{
+    const float t = expf(-fabsf(g));
+    return (g < 0.0f ? t : 1.0f) / (1.0f + t) * g * u;
+}
+
+}  // namespace qg

@@ -5,7 +5,9 @@
  * from the same 4-bit matrix, for AMD MI355X (gfx950); and the serving-step
  * operators between those products: a paged key/value cache held in 4 bits
  * with its page plan, append, read-back and attention, and the log
- * probabilities of given tokens (second part of this file).
+ * probabilities of given tokens (second part of this file); and microscaled
+ * (MX) numbers with their products and the router, sort and products of an
+ * experts' layer (third part).
  *
  * Notation. W is M x K (M outputs, K inputs). Activations x are float32
  * [rows][K], outputs y are float32 [rows][M]; every array is row-major and
@@ -479,6 +481,165 @@ int qlogprobs(const float *logits, int64_t ld, int64_t rows, int64_t vocab, cons
               float *logprob, float *entropy, int32_t *rank, int32_t *top_ids, float *top_logprobs,
               void *ws, size_t ws_bytes, hipStream_t stream);
 size_t qlogprobs_workspace_bytes(int64_t rows, int64_t vocab, int top);
+
+/* ------------------------------------------------------------------------
+ * Microscaled (MX) numbers and experts' layers
+ *
+ * MX rows hold blocks of 32 consecutive elements that share one scale byte s,
+ * which stands for 2^(s - 127); 255 makes the block NaN (OCP Microscaling
+ * Formats specification, version 1.0). The matrix cores take both as they lie
+ * in memory, so nothing is dequantized on the way.
+ *
+ *   QMX_E2M1  4 bits: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; byte j
+ *             of a row holds k = 2j in bits 0..3 and k = 2j+1 in bits 4..7
+ *   QMX_E4M3  8 bits: largest 448, no infinities
+ *
+ *   codes   uint8 [rows][K/2] or [rows][K], 16-byte aligned
+ *   scales  uint8 [rows][qmx_scale_pitch(K)], 4-byte aligned: K/32 bytes and
+ *           up to 3 of padding, whose contents do not matter
+ *   K is a multiple of 32, 32 <= K <= QMX_MAX_K.
+ *
+ * Weights are QMX_E2M1 (quantized once with qmx_quant, or brought along),
+ * activations either. An experts' layer of a decoder runs qmoe_route (or
+ * qmoe_plan, behind a router of one's own), qmx_quant, qmoe_gemm with
+ * QMX_SILU_MUL over the gate and up matrices, qmx_quant, qmoe_gemm over the
+ * down matrices without `order`, and qmoe_combine. The conventions of the top
+ * of this file hold; a call with 0 rows is valid (and writes offsets only).
+ * No entry point reads or writes out of its buffers for any contents of
+ * offsets, order, slots or ids.
+ * ------------------------------------------------------------------------ */
+
+typedef enum {
+    QMX_E2M1 = 1,
+    QMX_E4M3 = 2
+} qmx_format;
+
+typedef enum {
+    QMX_NONE = 0,
+    QMX_SILU_MUL = 1   /* gate / (1 + exp(-gate)) * up */
+} qmx_act;
+
+#define QMX_MAX_K (1 << 21)
+#define QMX_MAX_M (1 << 24)
+#define QMOE_MAX_EXPERTS 1024
+#define QMOE_MAX_TOP 32
+
+/* Bytes from a row of scales to the next: K/32 rounded up to a multiple of 4
+ * (0 for a K out of range). */
+int64_t qmx_scale_pitch(int64_t K);
+
+/*
+ * qmx_quant -- rows of activations (or weights) quantized into MX blocks.
+ * With E the exponent field of the block's largest magnitude (as float32),
+ *   s = max(E - emax, 0),  emax = 2 (QMX_E2M1) or 8 (QMX_E4M3),
+ * and each element is x * 2^(127 - s) rounded to the nearest element, ties to
+ * the even code, beyond the largest element to that one; the sign of a zero
+ * is kept. A block with a NaN or an infinity gets s = 255 and codes 0.
+ * Padding bytes of scales are written as 0.
+ *   x  rows of K elements of `dtype` (qg_dtype), x_stride elements apart
+ *      (x_stride >= K, a multiple of 16 bytes)
+ *   0 <= rows <= 2^31 - 1.
+ */
+int qmx_quant(int dtype, const void *x, int64_t x_stride, int64_t rows, int64_t K, int fmt,
+              void *codes, void *scales, hipStream_t stream);
+
+/*
+ * qmx_dequant -- the values that MX rows stand for: element * 2^(s - 127),
+ * exact in float32 (past its range infinity; from 2^-149 on down rounded), rounded to
+ * nearest even for QG_BF16. Blocks with s = 255 are quiet NaNs.
+ */
+int qmx_dequant(int fmt, const void *codes, const void *scales, int64_t rows, int64_t K,
+                int dtype, void *x, int64_t x_stride, hipStream_t stream);
+
+/*
+ * qmx_gemm -- product of MX rows with MX weights, from one row to long prompts.
+ *   y[n][m] = sum over k of x[n][k] * w[m][k],  0 <= n < N, 0 <= m < M,
+ * with QMX_SILU_MUL W has 2 M rows, and of g from rows 0..M-1 and u from rows
+ * M..2M-1, both float32 sums,  y = g / (1 + exp(-g)) * u.
+ * Products of elements and scales are exact; sums are float32, where an
+ * instruction adds the products of 64 or 128 inputs at once and keeps 24
+ * bits below the largest of them and the sum: every output is within
+ * (K / 32 + 4) * 2^-23 * sum_k |x w| of the exact sum before the activation
+ * and the rounding to `dtype`. A block with s = 255, or an e4m3 NaN, makes the
+ * outputs of its row (of x) or column (of W) NaN. Results repeat from call
+ * to call; the rounding of a row depends on how many rows there are.
+ *   xfmt   QMX_E2M1 or QMX_E4M3;  W is QMX_E2M1
+ *   y      `dtype` [N][M], 16-byte aligned
+ *   1 <= M <= QMX_MAX_M, 0 <= N <= 2^31 - 1, the tiles of a launch below 2^24
+ *   (QG_ERR_SHAPE).
+ * Workspace: qmx_gemm_workspace_bytes(...) for the same arguments (partial
+ * sums where few rows leave too few tiles and K is split).
+ */
+int qmx_gemm(int xfmt, const void *x_codes, const void *x_scales, const void *w_codes,
+             const void *w_scales, int act, int dtype, void *y, int64_t M, int64_t K, int64_t N,
+             void *ws, size_t ws_bytes, hipStream_t stream);
+size_t qmx_gemm_workspace_bytes(int xfmt, int act, int64_t M, int64_t K, int64_t N);
+
+/*
+ * qmoe_plan -- the pairs (token n, choice j), p = n * top + j, of tokens and
+ * their experts, sorted by expert.
+ *   ids      int32 [rows][top]; a pair whose id is outside [0, experts) has no
+ *            expert (none was to be had, or another GPU has it)
+ *   offsets  int32 [experts + 1]  places of expert e's pairs: offsets[e] ..
+ *            offsets[e + 1] - 1; within an expert pairs keep their order
+ *   order    int32 [rows * top]   the pair at each place; -1 behind the last
+ *   slots    int32 [rows][top]    the place of each pair; -1 for those of no
+ *            expert
+ *   0 <= rows, rows * top <= 2^31 - 1, 1 <= top <= min(experts, QMOE_MAX_TOP),
+ *   experts <= QMOE_MAX_EXPERTS.
+ * Workspace: qmoe_plan_workspace_bytes(...).
+ */
+int qmoe_plan(const int32_t *ids, int64_t rows, int experts, int top, int32_t *offsets,
+              int32_t *order, int32_t *slots, void *ws, size_t ws_bytes, hipStream_t stream);
+size_t qmoe_plan_workspace_bytes(int64_t rows, int experts, int top);
+
+/*
+ * qmoe_route -- the best `top` experts of each row of a router's logits, with
+ * their softmax weights, and the plan of their pairs (as qmoe_plan).
+ *   ids[n][j]      the j-th expert of row n in the order of larger logits
+ *                  first, ties by lower index (-0 equals +0), among logits
+ *                  above -infinity; -1 where there are fewer than top
+ *   weights[n][j]  exp(x - L), L = log sum exp over all experts, or with
+ *                  renorm = 1 over the chosen ones; 0 where ids is -1
+ * A row with a NaN or +infinity has ids -1 and weights NaN.
+ *   logits  `dtype` rows, ld >= experts elements apart, aligned to an element
+ */
+int qmoe_route(int dtype, const void *logits, int64_t ld, int64_t rows, int experts, int top,
+               int renorm, int32_t *ids, float *weights, int32_t *offsets, int32_t *order,
+               int32_t *slots, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * qmoe_gemm -- qmx_gemm of each expert over its rows of a plan.
+ *   y[s][m] = sum over k of x[r(s)][k] * w[e(s)][m][k]   (or with QMX_SILU_MUL
+ *   as there), for places s < offsets[experts]; rows of y behind are left as
+ *   they were.
+ *   order  r(s) = order[s] / top: x has `rows` rows, gathered on the way; or
+ *          NULL, r(s) = s: x has rows * top rows in the plan's order. An entry
+ *          outside [0, rows * top) stands for a row of zeros. With order, x_codes
+ *          is at most 2^31 - 1 bytes (QG_ERR_SHAPE).
+ *   W      QMX_E2M1, the experts' matrices one behind the other: M (or 2 M)
+ *          rows each
+ *   y      `dtype` [rows * top][M]
+ *   offsets that are no plan's (not rising, outside [0, rows * top]): any rows
+ *   of y may hold anything.
+ * Sizes as qmx_gemm and qmoe_plan. Workspace: qmoe_gemm_workspace_bytes(...).
+ */
+int qmoe_gemm(int xfmt, const void *x_codes, const void *x_scales, const void *w_codes,
+              const void *w_scales, const int32_t *offsets, const int32_t *order, int64_t rows,
+              int experts, int top, int act, int dtype, void *y, int64_t M, int64_t K, void *ws,
+              size_t ws_bytes, hipStream_t stream);
+size_t qmoe_gemm_workspace_bytes(int xfmt, int act, int64_t rows, int experts, int top, int64_t M,
+                                 int64_t K);
+
+/*
+ * qmoe_combine -- the experts' rows back to their tokens, weighted.
+ *   out[n][m] = sum over j of weights[n][j] * y[slots[n][j]][m], in float32 and
+ *   in the order of j; a slot outside [0, rows * top) adds weights[n][j] * 0 (so
+ *   that a row the router could not read is NaN, and not silently 0).
+ *   y  `dtype` [rows * top][M];  out  `out_dtype` [rows][M];  1 <= M <= QMX_MAX_M.
+ */
+int qmoe_combine(int dtype, const void *y, const int32_t *slots, const float *weights, int64_t rows,
+                 int top, int64_t M, int out_dtype, void *out, hipStream_t stream);
 
 /* Static text for a status code. */
 const char *qg_status_str(int status);
