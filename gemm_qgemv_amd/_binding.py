@@ -26,7 +26,7 @@ QG_MAX_PLAN_BATCH = 8192
 QG_MAX_TOP = 64
 QMX_E2M1, QMX_E4M3 = 1, 2
 QMX_NONE, QMX_SILU_MUL = 0, 1
-QMX_MAX_K, QMX_MAX_M = 1 << 21, 1 << 24
+QMX_MAX_K, QMX_MAX_M = 1 << 21, 1 << 23
 QMOE_MAX_EXPERTS, QMOE_MAX_TOP = 1024, 32
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqg.so")

@@ -92,27 +92,25 @@ __device__ __forceinline__ uint32_t mx_in_or_out(uint32_t off, int i, int n)
     return off | out;
 }
 
-// y[n] for four outputs side by side, of float32 or bf16 (`vec`: the address
-// is a multiple of four elements).
-__device__ __forceinline__ void put4(float *dst, const float (&v)[4], int n, bool vec)
+// The wave's LDS accesses before this come before those after it.
+__device__ __forceinline__ void wave_order()
 {
-    if (vec && n >= 4) {
-        *reinterpret_cast<f32x4 *>(dst) = f32x4{v[0], v[1], v[2], v[3]};
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < n) dst[i] = v[i];
-    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
-__device__ __forceinline__ void put4(uint16_t *dst, const float (&v)[4], int n, bool vec)
+
+// The value, computed where this stands: what follows from it is not kept in
+// registers over the loops around.
+__device__ __forceinline__ int mx_here(int v)
 {
-    if (vec && n >= 4) {
-        *reinterpret_cast<u32x2 *>(dst) = u32x2{f32_to_bf16_pair(v[0], v[1]), f32_to_bf16_pair(v[2], v[3])};
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < n) dst[i] = static_cast<uint16_t>(f32_to_bf16_bits(v[i]));
-    }
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+__device__ __forceinline__ int mx_here_scalar(int v)
+{
+    asm volatile("" : "+s"(v));
+    return v;
 }
 
 }  // namespace qg

@@ -44,7 +44,7 @@ struct MxGemmParams {
     int64_t N;               // rows (grouped: pairs)
     int32_t K, pitch;        // inputs a row, bytes of a row of scales
     int32_t tiles_m, tiles_n;
-    bool vec;                // M is a multiple of 4
+    int64_t ws_rows;         // tiles: rows of the weights' scales, which are laid out for them, as x's are
     // grouped only
     const int32_t *offsets;  // [experts + 1]
     const int32_t *order;    // pair of each sorted row, or NULL: x lies sorted
@@ -96,35 +96,37 @@ constexpr int kMaxExperts = 1024;
 template <int T>
 __device__ __forceinline__ GroupTile group_tile(const int32_t *offsets, int experts, int64_t pairs, int item)
 {
-    constexpr int C = kMaxExperts / 64;
-    const int lane = threadIdx.x & 63, c = (experts + 63) >> 6, first = lane * c;
-    int o[C + 1];
+    constexpr int C = 4;                             // offsets under way together
+    const int lane = mx_here(threadIdx.x & 63), c = (experts + 63) >> 6, first = lane * c;
+    const int most = static_cast<int>(pairs);
+    // f(expert, first row, rows) for the lane's experts in order
+    const auto each = [&](auto f) {
+        for (int j0 = 0; j0 < c; j0 += C) {
+            int o[C + 1];
 #pragma unroll
-    for (int j = 0; j <= C; ++j)
-        if (j <= c) o[j] = offsets[min(first + j, experts)];
-    int mine = 0;
+            for (int j = 0; j <= C; ++j) o[j] = offsets[min(first + min(j0 + j, c), experts)];
 #pragma unroll
-    for (int j = 0; j <= C; ++j)
-        if (j <= c) {
-            o[j] = static_cast<int>(max(int64_t(0), min(int64_t(o[j]), pairs)));
-            if (j > 0) mine += (max(o[j] - o[j - 1], 0) + (T - 1)) / T;
+            for (int j = 0; j <= C; ++j) o[j] = max(0, min(o[j], most));
+#pragma unroll
+            for (int j = 0; j < C; ++j) f(first + j0 + j, o[j], max(o[j + 1] - o[j], 0));
         }
+    };
+    int mine = 0;
+    each([&](int, int, int n) { mine += (n + (T - 1)) / T; });
     const int upto = wave_inclusive_sum32(mine);
     const uint64_t after = __ballot(upto > item);
     if (after == 0) return GroupTile{-1, 0, 0};
     int rest = item - (upto - mine);
     GroupTile t{0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < C; ++j)
-        if (j < c) {
-            const int n = max(o[j + 1] - o[j], 0), tiles = (n + (T - 1)) / T;
-            if (rest >= 0 && rest < tiles) {
-                t.e = first + j;
-                t.r0 = o[j] + rest * T;
-                t.r1 = min(t.r0 + T, o[j] + n);
-            }
-            rest -= tiles;
+    each([&](int e, int r0, int n) {
+        const int tiles = (n + (T - 1)) / T;
+        if (rest >= 0 && rest < tiles) {
+            t.e = e;
+            t.r0 = r0 + rest * T;
+            t.r1 = min(t.r0 + T, r0 + n);
         }
+        rest -= tiles;
+    });
     const int owner = __builtin_ctzll(after);
     t.e = __builtin_amdgcn_readlane(t.e, owner);
     t.r0 = __builtin_amdgcn_readlane(t.r0, owner);
@@ -145,11 +147,24 @@ __device__ __forceinline__ int64_t x_row(const MxGemmParams &p, int64_t r0, int 
     return row < p.x_rows ? row : -1;
 }
 
-// g / (1 + exp(-g)) * u, with the exponential of a negative number only (it does not overflow).
+// g / (1 + exp(-g)) * u. With t = exp(-|g|), which does not overflow, the factor is
+// 1 / (1 + t), or t / (1 + t) where g < 0. t = 2^p (1 + e ln 2), p the float32
+// nearest -|g| log2(e) and e what that leaves out; below 2^-64 it is held times
+// 2^64 (p + 64 is exact there), and the reciprocal of 1..2 is refined once: 8
+// roundings in all.
 __device__ __forceinline__ float silu_mul(float g, float u)
 {
-    const float t = expf(-fabsf(g));
-    return (g < 0.0f ? t : 1.0f) / (1.0f + t) * g * u;
+    constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+    const float a = fminf(fabsf(g), 200.0f), p = a * -kLog2e;
+    const float e = fmaf(a, -kLog2eLow, fmaf(a, -kLog2e, -p));
+    const bool tiny = p < -64.0f;
+    const float size = tiny ? 0x1p-64f : 1.0f;
+    float t = __builtin_amdgcn_exp2f(tiny ? p + 64.0f : p);
+    t = fmaf(t, e * kLn2, t);
+    const float d = fmaf(t, size, 1.0f);
+    float q = __builtin_amdgcn_rcpf(d);
+    q = fmaf(fmaf(-d, q, 1.0f), q, q);
+    return g < 0.0f ? t * q * g * u * size : q * g * u;
 }
 
 }  // namespace qg

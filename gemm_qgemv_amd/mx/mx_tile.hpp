@@ -1,15 +1,19 @@
 // mx_tile.hpp -- MX products for many rows: tiles of weights and activations
 // brought from memory straight into LDS.
 //
-// A workgroup of WM x WN waves takes BM weight rows and BN rows of x; a stage
-// is 256 inputs of both, with their scales, in one of two LDS buffers, filled
-// by loads that go to LDS directly while the other is multiplied. A wave takes
-// BM / WM x BN / WN of the tile in blocks of 32 x 32.
+// A workgroup of WM x WN waves takes tiles of BM weight rows and BN rows of x in
+// turn; a stage is 256 inputs of both in one of D LDS slots, filled by loads
+// that go to LDS directly while others are multiplied. A wave takes BM / WM x BN
+// / WN of the tile in blocks of 32 x 32. Stages run on from tile to tile: while
+// a tile's results are written the next one's first stages are on their way.
 //
 // Which inputs an instruction takes together is free as long as both operands
-// agree: of the stage's 8 blocks a lane with g = 0 takes blocks 0..3 in turn, one
-// with g = 1 blocks 4..7. So its scales of the whole stage are the four bytes
-// of one dword, and the instruction's byte selector walks them.
+// agree: of a stage's 8 blocks a lane with g = 0 takes blocks 0..3 in turn, one
+// with g = 1 blocks 4..7. So its scales of the stage are the four bytes of one
+// dword, and the instruction's byte selector walks them. Scales are laid out stage
+// by stage first (mx_scales_kernel): of a row's line of scales a stage needs 8
+// bytes, and a load costs by the lines it touches (fetched from the rows as they
+// are, scales cost half as much as all codes).
 //
 // With SILU the tile's weight rows are 32 of the gate and 32 of the up matrix
 // in turn, so that a lane holds both numbers of an output.
@@ -20,12 +24,15 @@
 namespace qg {
 
 constexpr int kTileK = 256;      // inputs of a stage
+constexpr int kTileScale = kTileK / kMxBlock;      // bytes of scales of a row and stage
 
-template <int XF, int BM, int BN>
+template <int XF, int BM, int BN, int NW, int D>
 struct MxTileLds {
-    static constexpr int wrow = kTileK / 2, xrow = static_cast<int>(mx_bytes<XF>(kTileK)), srow = kTileK / 32;
-    static constexpr int x = BM * wrow, s = x + BN * xrow, stage = s + (BM + BN) * srow;
-    static constexpr int bytes = 2 * stage;
+    static constexpr int wrow = kTileK / 2, xrow = static_cast<int>(mx_bytes<XF>(kTileK));
+    static constexpr int wb = (BM + 127) / 128, xb = (BN + 127) / 128;    // loads of scales: 128 rows, 1 KiB
+    static constexpr int x = BM * wrow, sw = x + BN * xrow, sx = sw + wb * 1024, stage = sx + xb * 1024;
+    static constexpr int table = D * stage;                               // grouped: the rows of x behind a tile's
+    static constexpr int bytes = table + BN * 4;
 };
 
 // 16-byte chunk c of LDS row r lies at chunk c ^ swizzle(r): 16 lanes that
@@ -36,197 +43,406 @@ __device__ __forceinline__ int mx_swizzle(int r)
     return CHUNKS == 16 ? r & 15 : (r & 7) ^ ((r >> 3) & 1);
 }
 
-template <int S, int XF, int TI, int TJ>
-__device__ __forceinline__ void mx_tile_step(const uint8_t *wl, const uint8_t *xl, const int (&sw)[TI], const int (&sx)[TJ],
-                                             f32x16 (&acc)[TI][TJ], int r, int g)
-{
-    constexpr int wrow = kTileK / 2, xrow = static_cast<int>(mx_bytes<XF>(kTileK));
-    // (the swizzle goes by a row's low four bits, which r has)
-    constexpr int XP = kXParts<XF>;
-    i32x8 a[TI], b[TJ][XP];
+// The operands of one step (64 inputs) of a wave, from LDS (wl and xl: its first rows).
+template <int XF, int TI, int TJ>
+struct MxTileOps {
+    static constexpr int XP = kXParts<XF>;
+    u32x4 a[TI], b[TJ][XP];
+
+    __device__ __forceinline__ void read(const uint8_t *wl, const uint8_t *xl, int s, int r, int g)
+    {
+        constexpr int wrow = kTileK / 2, xrow = static_cast<int>(mx_bytes<XF>(kTileK));
+        // (the swizzle goes by a row's low four bits, which r has)
 #pragma unroll
-    for (int i = 0; i < TI; ++i) {
-        const int row = 32 * i + r;
-        const u32x4 v = *reinterpret_cast<const u32x4 *>(wl + row * wrow + 16 * ((4 * g + S) ^ mx_swizzle<8>(row)));
-        a[i] = i32x8{int(v[0]), int(v[1]), int(v[2]), int(v[3]), 0, 0, 0, 0};
-    }
+        for (int i = 0; i < TI; ++i)
+            a[i] = *reinterpret_cast<const u32x4 *>(wl + (32 * i + r) * wrow + 16 * ((4 * g + s) ^ mx_swizzle<8>(r)));
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-        const int row = 32 * j + r;
-        if constexpr (XF == kMxE2M1) {
-            const u32x4 v = *reinterpret_cast<const u32x4 *>(xl + row * xrow + 16 * ((4 * g + S) ^ mx_swizzle<8>(row)));
-            x_operands<XF>(v, v, b[j]);
-        } else {
-            // bytes 0..15: half g of block S; bytes 16..31: half g of block 4 + S
-            const u32x4 u = *reinterpret_cast<const u32x4 *>(xl + row * xrow + 16 * ((2 * S + g) ^ mx_swizzle<16>(row)));
-            const u32x4 v = *reinterpret_cast<const u32x4 *>(xl + row * xrow + 16 * ((8 + 2 * S + g) ^ mx_swizzle<16>(row)));
-            x_operands<XF>(u, v, b[j]);
+        for (int j = 0; j < TJ; ++j) {
+            const uint8_t *row = xl + (32 * j + r) * xrow;
+            if constexpr (XF == kMxE2M1) {
+                b[j][0] = *reinterpret_cast<const u32x4 *>(row + 16 * ((4 * g + s) ^ mx_swizzle<8>(r)));
+            } else {
+                // bytes 0..15: half g of block s; bytes 16..31: half g of block 4 + s
+                b[j][0] = *reinterpret_cast<const u32x4 *>(row + 16 * ((2 * s + g) ^ mx_swizzle<16>(r)));
+                b[j][1] = *reinterpret_cast<const u32x4 *>(row + 16 * ((8 + 2 * s + g) ^ mx_swizzle<16>(r)));
+            }
         }
     }
+};
+
+template <int S, int XF, int TI, int TJ>
+__device__ __forceinline__ void mx_tile_step(const MxTileOps<XF, TI, TJ> &o, const int (&sw)[TI], const int (&sx)[TJ],
+                                             f32x16 (&acc)[TI][TJ])
+{
+    constexpr int XP = kXParts<XF>;
+    i32x8 b[TJ][XP];
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) x_operands<XF>(o.b[j][0], o.b[j][XP - 1], b[j]);
 #pragma unroll
     for (int h = 0; h < XP; ++h)
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+            const i32x8 a = {int(o.a[i][0]), int(o.a[i][1]), int(o.a[i][2]), int(o.a[i][3]), 0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < TJ; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b[j][h], acc[i][j], kMxE2M1, XF, S, sw[i], S, sx[j]);
+        }
+}
+
+// The instructions since the last of these in the order wanted: LDS reads (and
+// LOADS loads to LDS) spread between the matrix instructions. Left alone the
+// compiler puts every read right before its use, and the matrix cores wait.
+template <int MFMAS, int READS, int LOADS>
+__device__ __forceinline__ void mx_interleave()
+{
+    constexpr int slots = MFMAS < READS ? MFMAS : READS;
+#pragma unroll
+    for (int i = 0; i < slots; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, READS / slots, 0);                      // LDS reads
+        if (LOADS / slots) __builtin_amdgcn_sched_group_barrier(0x020, LOADS / slots, 0);   // loads
+        __builtin_amdgcn_sched_group_barrier(0x008, MFMAS / slots, 0);                      // matrix instructions
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// This wave's LDS reads are done, all but the last N of its memory operations too;
+// then all waves of the workgroup meet. (One block, so that nothing moves between.)
+template <int N>
+__device__ __forceinline__ void mx_meet()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// A wave's part of a tile to memory: rows from n0 on of the tile's, outputs from
+// m0 on. D: column r is a row of x, element v the weight row 8 (v / 4) + 4 g + v % 4; of
+// bf16 two lanes of a row trade half of theirs, so that each stores 16 bytes side
+// by side. Without branches (what lies outside goes to offsets out of range): cut
+// into blocks, the compiler moves the accumulators about before it stores them.
+// LINES: rows of y are whole pieces of 16 bytes.
+template <typename T, bool SILU, bool LINES, int TI, int TJ>
+__device__ __forceinline__ void mx_tile_store(const f32x16 (&acc)[TI][TJ], T *y, int64_t M, int rows, int outs, int n0, int m0)
+{
+    constexpr int WI = SILU ? 2 : 1, SIZE = static_cast<int>(sizeof(T));
+    const int lane = mx_here(threadIdx.x & 63), r = lane & 31, g = lane >> 5;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+        const auto buf = mx_buffer(y + (n0 + 32 * j) * M, 32 * M * SIZE);
+        const uint32_t row = n0 + 32 * j + r < rows ? static_cast<uint32_t>(r * M * SIZE) : kMxOut;
+#pragma unroll
+        for (int i = 0; i < TI; i += WI) {
+            const int mb = m0 + 32 * i / WI;
+            __builtin_amdgcn_sched_barrier(0);
+            float out[16];
+#pragma unroll
+            for (int v = 0; v < 16; ++v) out[v] = SILU ? silu_mul(acc[i][j][v], acc[i + WI - 1][j][v]) : acc[i][j][v];
+            if constexpr (SIZE == 4) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int m = mb + 8 * q + 4 * g;
+                    if constexpr (LINES) {
+                        const f32x4 v = {out[4 * q], out[4 * q + 1], out[4 * q + 2], out[4 * q + 3]};
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), buf, m < outs ? row + m * 4 : kMxOut, 0, 0);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(out[4 * q + e]), buf, m + e < outs ? row + (m + e) * 4 : kMxOut, 0, 0);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; q += 2) {
+                    // this lane's outputs 8 q + 4 g .. and 8 (q + 1) + 4 g ..
+                    u32x2 lo, hi;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const auto t = __builtin_amdgcn_permlane32_swap(f32_to_bf16_pair(out[4 * q + 2 * e], out[4 * q + 2 * e + 1]),
+                                                                        f32_to_bf16_pair(out[4 * q + 4 + 2 * e], out[4 * q + 5 + 2 * e]), false, false);
+                        lo[e] = t[0], hi[e] = t[1];
+                    }
+                    // now 8 (q + g) .. + 7
+                    const int m = mb + 8 * (q + g);
+                    const u32x4 v = {lo[0], lo[1], hi[0], hi[1]};
+                    if constexpr (LINES) {
+                        __builtin_amdgcn_raw_buffer_store_b128(v, buf, m < outs ? row + m * 2 : kMxOut, 0, 0);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(v[e / 2] >> (16 * (e & 1))), buf,
+                                                                  m + e < outs ? row + (m + e) * 2 : kMxOut, 0, 0);
+                    }
+                }
+            }
+        }
+    }
+}
+
+// A tile: rows r0 .. r0 + rows - 1 of expert e, outputs from m0 on.
+struct MxTile {
+    int r0, m0, e, rows;      // rows 0: none
+};
+
+// Scales of rows as the tiles take them: [stage][row][8], zeros behind a row's
+// end. Weights' rows, then x's, which with `order` are those of the sorted pairs.
+struct MxScalesParams {
+    const uint8_t *ws, *xs;
+    uint8_t *to_w, *to_x;
+    int64_t wrows, xrows;     // x: rows of the product
+    int32_t wblocks;          // workgroups that take weights' rows
+    int32_t pitch, blocks;    // bytes of a row, of these scales
+    int32_t stages;
+    const int32_t *order;
+    int64_t x_rows;           // rows that may be gathered
+    FastDiv top;
+};
+
+constexpr int kScaleThreads = 256;
+
+__device__ __forceinline__ void mx_scales_rows(const MxScalesParams &p, const uint8_t *from, uint8_t *to, int64_t rows, int64_t first, bool gather)
+{
+    // lanes along rows: stores side by side; a row's line is read by one lane stage after stage
+    const int64_t row = first + (threadIdx.x & 63);
+    if (row >= rows) return;
+    int64_t at = row;
+    if (gather) {
+        const int64_t pair = p.order[row];
+        at = pair < 0 || pair >= rows ? -1 : static_cast<uint32_t>(pair) / p.top;
+        if (at >= p.x_rows) at = -1;
+    }
+    for (int t = threadIdx.x >> 6; t < p.stages; t += kScaleThreads / 64) {
+        uint32_t v[2];
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+            const int b = t * 8 + 4 * d, left = p.blocks - b;
+            v[d] = at >= 0 && left > 0 ? *reinterpret_cast<const uint32_t *>(from + at * p.pitch + b) : 0;
+            if (left < 4) v[d] &= left <= 0 ? 0 : (1u << (8 * left)) - 1;
+        }
+        *reinterpret_cast<u32x2 *>(to + (t * rows + row) * 8) = u32x2{v[0], v[1]};
+    }
+}
+
+static __global__ __launch_bounds__(kScaleThreads) void mx_scales_kernel(MxScalesParams p)
+{
+    if (static_cast<int>(blockIdx.x) < p.wblocks)
+        mx_scales_rows(p, p.ws, p.to_w, p.wrows, int64_t(blockIdx.x) * 64, false);
+    else
+        mx_scales_rows(p, p.xs, p.to_x, p.xrows, int64_t(blockIdx.x - p.wblocks) * 64, p.order != nullptr);
+}
+
+template <int XF, typename T, bool SILU, bool GROUPED, int BM, int BN, int WM, int WN, int D>
+__global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
+{
+    constexpr int NW = WM * WN, TI = BM / WM / 32, TJ = BN / WN / 32, WI = SILU ? 2 : 1;
+    using L = MxTileLds<XF, BM, BN, NW, D>;
+    static_assert(TI % WI == 0, "a wave holds gate and up rows of an output");
+    constexpr int OUTS = BM / WI;                    // outputs of a tile
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 31, g = lane >> 5;
+    const int wrb = p.K / 2, xrb = static_cast<int>(mx_bytes<XF>(p.K));
+    const int stages = (p.K + kTileK - 1) / kTileK;
+    const bool gather = GROUPED && p.order;
+
+    // Consecutive workgroups go to the 8 XCDs in turn: each XCD gets a run of
+    // tiles, which its workgroups take in turn, in bands of 4 tiles of rows, these
+    // first: the 32 tiles that an XCD's compute units work on are 8 x 4, 12
+    // operands for 33 in a row.
+    int nth = blockIdx.x >> 3;
+    const auto next_tile = [&]() {
+        const int ntiles = p.tiles_m * p.tiles_n, xcd = blockIdx.x & 7, xcds = min(8, static_cast<int>(gridDim.x));
+        const int run = ntiles / xcds + (xcd < ntiles % xcds), run0 = xcd * (ntiles / xcds) + min(xcd, ntiles % xcds);
+        MxTile t{0, 0, 0, 0};
+        while (nth < run) {
+            constexpr int BAND = 4;
+            const int id = run0 + nth;
+            nth += (gridDim.x - xcd + 7) >> 3;       // workgroups of this XCD
+            const int band = id / (BAND * p.tiles_m), in = id - band * (BAND * p.tiles_m);
+            const int high = min(BAND, p.tiles_n - band * BAND);
+            const int tm = in / high, tn = band * BAND + in % high;
+            t.m0 = tm * OUTS;
+            if constexpr (GROUPED) {
+                const GroupTile u = group_tile<BN>(p.offsets, p.experts, p.N, tn);
+                if (u.e < 0) continue;
+                t.e = u.e, t.r0 = u.r0, t.rows = u.r1 - u.r0;
+            } else {
+                t.r0 = tn * BN;
+                t.rows = static_cast<int>(min(int64_t(BN), p.N - t.r0));
+            }
+            break;
+        }
+        return t;
+    };
+
+    // This lane's pieces of a stage. Weights: load i of the wave fills 8 LDS rows
+    // from 8 q on, q = i * NW + wave; x likewise; scales 128 rows, two a lane.
+    constexpr int WL = BM / 8 / NW, XR = 1024 / L::xrow, XL = BN / XR / NW, XC = L::xrow / 16;
+    constexpr int SB = L::wb + L::xb;
+    static_assert(SB <= NW, "a load of scales a wave");
+    const int sload = wave % SB;                     // (two waves may have the same)
+    const bool sofw = sload < L::wb;
+    static_assert(WL * NW * 8 == BM && XL * NW * XR == BN, "whole loads");
+    const auto weight_row = [&](int row) { return SILU ? (row >> 6) * 32 + (row & 31) : row; };
+    // the row of x's load i that this lane fills, and the piece of it
+    const auto x_lds_row = [&](int lane, int i) { return XR * (i * NW + wave) + lane / XC; };
+    const auto x_piece = [&](int lane, int i) { return (lane % XC) ^ mx_swizzle<XC>(x_lds_row(lane, i)); };
+    // the tile that is being loaded, and its next stage
+    int at = 0;
+    uint32_t *row_table = reinterpret_cast<uint32_t *>(lds + L::table) + wave * (BN / NW);
+    const uint8_t *wbase[WI], *xbase;
+    int wlen, xlen;
+    // this wave's load of scales: rows behind `sbase` of those laid out
+    const uint8_t *sbase;
+    int64_t srows;           // rows of a stage
+    int slen;
+    const auto open = [&](const MxTile &t) {
+        const int lane = mx_here(threadIdx.x & 63);
+        at = 0;
+        const int outs = min(OUTS, static_cast<int>(p.M) - t.m0);
+#pragma unroll
+        for (int i = 0; i < WI; ++i) wbase[i] = p.wc + ((int64_t(t.e) * WI + i) * p.M + t.m0) * wrb;
+        wlen = outs * wrb;
+        const int64_t first = gather ? 0 : t.r0, in = gather ? p.x_rows : t.rows;
+        xbase = p.xc + first * xrb;
+        xlen = static_cast<int>(in * xrb);
+        // (of the weights' scales the up matrix's come after all of the gate's)
+        const int64_t srow = sofw ? int64_t(t.e) * WI * p.M + t.m0 + 128 / WI * sload : t.r0 + 128 * (sload - L::wb);
+        sbase = (sofw ? p.ws : p.xs) + srow * kTileScale;
+        srows = sofw ? p.ws_rows : p.N;
+        slen = static_cast<int>(max(min(srows - srow, sofw ? (WI - 1) * p.M + OUTS : int64_t(BN)), int64_t(0)) * kTileScale);
+        if constexpr (GROUPED) {
+            // where the rows that this wave's loads take begin, one a lane, kept in LDS for all of the tile's stages
+            static_assert(BN / NW <= 64, "a lane a row");
+            if (lane < BN / NW) {
+                const int64_t x = x_row<true>(p, t.r0, t.rows, XR * (lane / XR * NW + wave) + lane % XR);
+                row_table[lane] = x < 0 ? kMxOut : static_cast<uint32_t>(x * xrb);
+            }
+            wave_order();
+        }
+    };
+    const auto fill = [&](uint8_t *dst, bool real) {
+        const int wk = at * L::wrow, xk0 = at * L::xrow;
+        const int wrb = mx_here_scalar(p.K / 2), xrb = static_cast<int>(mx_bytes<XF>(mx_here_scalar(p.K)));
+        const int left = p.K - at * kTileK, lane = mx_here(threadIdx.x & 63);
+        __amdgpu_buffer_rsrc_t wbuf[WI];
+#pragma unroll
+        for (int i = 0; i < WI; ++i) wbuf[i] = mx_buffer(wbase[i] + wk, real ? wlen - wk : 0);
+        const auto xbuf = mx_buffer(xbase + xk0, real ? xlen - xk0 : 0);
+        // Within a load rows lie side by side, so that a lane has one offset for all of
+        // the weights' (the swizzle goes by a row's low four bits, and NW is even).
+        const uint32_t woff = static_cast<uint32_t>((lane >> 3) * wrb + 16 * ((lane & 7) ^ mx_swizzle<8>(8 * wave + (lane >> 3))));
+#pragma unroll
+        for (int i = 0; i < WL; ++i) {
+            const int q = i * NW + wave, part = SILU ? (q >> 2) & 1 : 0;
+            mx_to_lds16(wbuf[part], dst + q * 1024, woff + weight_row(8 * q) * wrb);
+        }
+        // inputs behind the row's end are zeros (the weights' there are any finite numbers)
+#pragma unroll
+        for (int i = 0; i < XL; ++i) {
+            const int q = i * NW + wave, piece = x_piece(lane, i);
+            const uint32_t row = GROUPED ? row_table[XR * i + lane / XC] : static_cast<uint32_t>(lane / XC * xrb + XR * q * xrb);
+            mx_to_lds16(xbuf, dst + L::x + q * 1024, piece * (XF == kMxE2M1 ? 32 : 16) < left ? row + 16 * piece : kMxOut);
+        }
+        // two rows of the weights' LDS rows, or of x's
+        const int srow = 2 * lane;
+        const uint32_t soff = static_cast<uint32_t>((sofw ? weight_row(srow) + (SILU && (srow & 32) ? p.M : 0) : srow) * kTileScale);
+        mx_to_lds16(mx_buffer(sbase + at * srows * kTileScale, real ? slen : 0), dst + L::sw + sload * 1024, soff);
+    };
+
+    f32x16 acc[TI][TJ];
+    const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
+    int sw[2][TI], sx[2][TJ];
+    MxTileOps<XF, TI, TJ> ops[2];
+    // step 0 of the stage in a slot and the stage's scales
+    const auto begin = [&](int slot, int (&w)[TI], int (&x)[TJ]) {
+        const uint8_t *src = lds + slot * L::stage, *swsrc = src + L::sw + 4 * g, *sxsrc = src + L::sx + 4 * g;
+#pragma unroll
+        for (int i = 0; i < TI; ++i) w[i] = *reinterpret_cast<const int *>(swsrc + (wm + 32 * i + r) * kTileScale);
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) x[j] = *reinterpret_cast<const int *>(sxsrc + (wn + 32 * j + r) * kTileScale);
+        ops[0].read(src + wm * L::wrow, src + L::x + wn * L::xrow, 0, r, g);
+    };
+
+    // tiles that are loaded, at least in part, behind the current one
+    MxTile cur = next_tile(), ahead[D];
+    if (cur.rows == 0) return;
+    int waiting = 0;
+    bool more = true;
+    open(cur);
+    // takes the next stage's tile
+    const auto advance = [&]() {
+        if (more && at == stages) {
+            const MxTile t = next_tile();
+            more = t.rows != 0;
+            if (more) {
+                open(t);
+#pragma unroll
+                for (int i = 0; i < D; ++i)
+                    if (i == waiting) ahead[i] = t;
+                ++waiting;
+            }
+        }
+    };
+    for (int d = 0; d < D; ++d) {
+        advance();
+        fill(lds + d * L::stage, more);
+        at += more;
+    }
+    mx_meet<0>();
+    begin(0, sw[0], sx[0]);
+
+    // A step's operands are read while the one before is multiplied. Once the
+    // last step's are read the waves meet: then the next stage's first operands
+    // are read and the stage's slot is filled anew, beside the last step's products.
+    constexpr int MFMAS = TI * TJ * kXParts<XF>, READS = TI + TJ * kXParts<XF>;
+    int slot = 0;
+    for (;;) {
 #pragma unroll
         for (int i = 0; i < TI; ++i)
 #pragma unroll
             for (int j = 0; j < TJ; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[i], b[j][h], acc[i][j], kMxE2M1, XF, S, sw[i], S, sx[j]);
-}
-
-template <int XF, typename T, bool SILU, bool GROUPED, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
-{
-    using L = MxTileLds<XF, BM, BN>;
-    constexpr int NW = WM * WN, TI = BM / WM / 32, TJ = BN / WN / 32, WI = SILU ? 2 : 1;
-    static_assert(TI % WI == 0, "a wave holds gate and up rows of an output");
-    extern __shared__ __align__(16) uint8_t lds[];
-
-    // consecutive workgroups go to the 8 XCDs in turn: each XCD gets a run of
-    // tiles, outputs first, which share rows of x in its L2
-    const int ntiles = p.tiles_m * p.tiles_n;
-    int bid = blockIdx.x;
-    {
-        const int each = ntiles >> 3, over = ntiles & 7, xcd = bid & 7, nth = bid >> 3;
-        bid = xcd * each + min(xcd, over) + nth;
-    }
-    const int tm = bid % p.tiles_m, tn = bid / p.tiles_m;
-    int64_t r0, e = 0;
-    int rows;
-    if constexpr (GROUPED) {
-        const GroupTile t = group_tile<BN>(p.offsets, p.experts, p.N, tn);
-        if (t.e < 0) return;
-        e = t.e, r0 = t.r0, rows = t.r1 - t.r0;
-    } else {
-        r0 = int64_t(tn) * BN;
-        rows = static_cast<int>(min(int64_t(BN), p.N - r0));
-    }
-    constexpr int OUTS = BM / WI;                    // outputs of a tile
-    const int64_t m0 = int64_t(tm) * OUTS;
-    const int outs = static_cast<int>(min(int64_t(OUTS), p.M - m0));
-    const int64_t wrb = p.K / 2, xrb = mx_bytes<XF>(p.K);
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 31, g = lane >> 5;
-
-    const bool gather = GROUPED && p.order;
-    const int64_t xfirst = gather ? 0 : r0, xin = gather ? p.x_rows : rows;
-    const uint8_t *wbase[WI], *wsbase[WI];
 #pragma unroll
-    for (int i = 0; i < WI; ++i) {
-        const int64_t row = (e * WI + i) * p.M + m0;
-        wbase[i] = p.wc + row * wrb;
-        wsbase[i] = p.ws + row * p.pitch;
-    }
-    const uint8_t *xbase = p.xc + xfirst * xrb, *xsbase = p.xs + xfirst * p.pitch;
-    const int64_t wlen = outs * wrb, wslen = int64_t(outs) * p.pitch, xlen = xin * xrb, xslen = xin * p.pitch;
-
-    // this lane's pieces of a stage. Weights: load i of the wave fills LDS rows 8 q .. 8 q + 7, q = i * NW + wave
-    constexpr int WL = BM / 8 / NW, XR = 1024 / L::xrow, XL = BN / XR / NW, XC = L::xrow / 16;
-    constexpr int SB = (BM + BN) / 32, SL = (SB + NW - 1) / NW;
-    static_assert(WL * NW * 8 == BM && XL * NW * XR == BN, "whole loads");
-    uint32_t woff[WL], xoff[XL], soff[SL];
-    int xk[XL];                                      // first input of the x piece within the stage
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+        for (int t = 0; t < stages; ++t) {
+            const uint8_t *wl = lds + slot * L::stage + wm * L::wrow, *xl = lds + slot * L::stage + L::x + wn * L::xrow;
+            __builtin_amdgcn_sched_barrier(0);
+            ops[1].read(wl, xl, 1, r, g);
+            mx_tile_step<0>(ops[0], sw[0], sx[0], acc);
+            mx_interleave<MFMAS, READS, 0>();
+            ops[0].read(wl, xl, 2, r, g);
+            mx_tile_step<1>(ops[1], sw[0], sx[0], acc);
+            mx_interleave<MFMAS, READS, 0>();
+            ops[1].read(wl, xl, 3, r, g);
+            mx_tile_step<2>(ops[0], sw[0], sx[0], acc);
+            mx_interleave<MFMAS, READS, 0>();
+            // (the first time all of the wave's stores of the last tile are waited for too)
+            if (D == 2 || t == 0)
+                mx_meet<0>();
+            else
+                mx_meet<(D - 2) * (WL + XL + 1)>();
+            const int freed = slot;
+            slot = slot + 1 == D ? 0 : slot + 1;
+            advance();
+            __builtin_amdgcn_sched_barrier(0);
+            begin(slot, sw[1], sx[1]);
+            fill(lds + freed * L::stage, more);
+            mx_tile_step<3>(ops[1], sw[0], sx[0], acc);
+            mx_interleave<MFMAS, READS + TI + TJ, WL + XL + 1>();
+            at += more;
 #pragma unroll
-    for (int i = 0; i < WL; ++i) {
-        const int row = 8 * (i * NW + wave) + (lane >> 3);
-        const int real = SILU ? (row >> 6) * 32 + (row & 31) : row;
-        woff[i] = static_cast<uint32_t>(real * wrb + 16 * ((lane & 7) ^ mx_swizzle<8>(row)));
-    }
+            for (int i = 0; i < TI; ++i) sw[0][i] = sw[1][i];
 #pragma unroll
-    for (int i = 0; i < XL; ++i) {
-        const int row = XR * (i * NW + wave) + lane / XC, chunk = (lane % XC) ^ mx_swizzle<XC>(row);
-        const int64_t at = x_row<GROUPED>(p, r0, rows, row);
-        xoff[i] = at < 0 ? kMxOut : static_cast<uint32_t>(at * xrb + 16 * chunk);
-        xk[i] = chunk * (XF == kMxE2M1 ? 32 : 16);
-    }
-#pragma unroll
-    for (int i = 0; i < SL; ++i) {
-        const int q = i * NW + wave, row = 32 * q + (lane >> 1);     // blocks of 32 rows, the weights' first
-        if (row < BM) {
-            soff[i] = static_cast<uint32_t>((SILU ? (row >> 6) * 32 + (row & 31) : row) * p.pitch + 4 * (lane & 1));
-        } else {
-            const int64_t at = row < BM + BN ? x_row<GROUPED>(p, r0, rows, row - BM) : -1;
-            soff[i] = at < 0 ? kMxOut : static_cast<uint32_t>(at * p.pitch + 4 * (lane & 1));
+            for (int j = 0; j < TJ; ++j) sx[0][j] = sx[1][j];
         }
-    }
-    const int stages = (p.K + kTileK - 1) / kTileK;
 
-    const auto fill = [&](int t, uint8_t *dst) {
-        const int64_t wk = int64_t(t) * L::wrow, xk0 = int64_t(t) * L::xrow, sk = int64_t(t) * L::srow;
-        const bool tail = (t + 1) * kTileK > p.K;
+        const int outs = min(OUTS, static_cast<int>(p.M) - cur.m0);
+        if (p.M % (16 / static_cast<int>(sizeof(T))) == 0)
+            mx_tile_store<T, SILU, true>(acc, static_cast<T *>(p.y) + int64_t(cur.r0) * p.M + cur.m0, p.M, cur.rows, outs, wn, wm / WI);
+        else
+            mx_tile_store<T, SILU, false>(acc, static_cast<T *>(p.y) + int64_t(cur.r0) * p.M + cur.m0, p.M, cur.rows, outs, wn, wm / WI);
+        if (waiting == 0) break;
+        cur = ahead[0];
 #pragma unroll
-        for (int i = 0; i < WL; ++i) {
-            const int q = i * NW + wave, part = SILU ? (q >> 2) & 1 : 0;
-            const auto buf = mx_buffer(wbase[part] + wk, wlen - wk);
-            mx_to_lds16(buf, dst + q * 1024, woff[i]);
-        }
-        const auto xbuf = mx_buffer(xbase + xk0, xlen - xk0);
-#pragma unroll
-        for (int i = 0; i < XL; ++i) {
-            // inputs behind the row's end are zeros (the weights' there are any finite numbers)
-            const uint32_t off = tail && t * kTileK + xk[i] >= p.K ? kMxOut : xoff[i];
-            mx_to_lds16(xbuf, dst + L::x + (i * NW + wave) * 1024, off);
-        }
-#pragma unroll
-        for (int i = 0; i < SL; ++i) {
-            const int q = i * NW + wave;
-            if (SL * NW != SB && q >= SB) break;
-            const bool ofw = 32 * q < BM;
-            const int part = SILU ? q & 1 : 0;
-            const auto buf = mx_buffer((ofw ? wsbase[part] : xsbase) + sk, (ofw ? wslen : xslen) - sk);
-            mx_to_lds4(buf, dst + L::s + q * 256, soff[i]);
-        }
-    };
-
-    f32x16 acc[TI][TJ];
-#pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-        for (int j = 0; j < TJ; ++j)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-    const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
-
-    const auto multiply = [&](int t, const uint8_t *src) {
-        // scale bytes behind the row's end count as 2^-127
-        const int left = p.K / 32 - t * (kTileK / 32) - 4 * g;
-        const uint32_t mask = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1;
-        int sw[TI], sx[TJ];
-#pragma unroll
-        for (int i = 0; i < TI; ++i)
-            sw[i] = static_cast<int>(*reinterpret_cast<const uint32_t *>(src + L::s + (wm + 32 * i + r) * L::srow + 4 * g) & mask);
-#pragma unroll
-        for (int j = 0; j < TJ; ++j)
-            sx[j] = static_cast<int>(*reinterpret_cast<const uint32_t *>(src + L::s + (BM + wn + 32 * j + r) * L::srow + 4 * g) & mask);
-        const uint8_t *wl = src + wm * L::wrow, *xl = src + L::x + wn * L::xrow;
-        mx_tile_step<0, XF, TI, TJ>(wl, xl, sw, sx, acc, r, g);
-        mx_tile_step<1, XF, TI, TJ>(wl, xl, sw, sx, acc, r, g);
-        mx_tile_step<2, XF, TI, TJ>(wl, xl, sw, sx, acc, r, g);
-        mx_tile_step<3, XF, TI, TJ>(wl, xl, sw, sx, acc, r, g);
-    };
-
-    fill(0, lds);
-    for (int t = 0; t < stages; ++t) {
-        __syncthreads();         // stage t has come, and nobody reads the other buffer any more
-        if (t + 1 < stages) fill(t + 1, lds + ((t + 1) & 1) * L::stage);
-        multiply(t, lds + (t & 1) * L::stage);
-    }
-
-    // D: column r is a row of x, element v the weight row 8 (v / 4) + 4 g + v % 4
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-        const int n = wn + 32 * j + r;
-        if (n >= rows) continue;
-        T *row = static_cast<T *>(p.y) + (r0 + n) * p.M + m0;
-#pragma unroll
-        for (int i = 0; i < TI; i += WI) {
-#pragma unroll
-            for (int v = 0; v < 16; v += 4) {
-                const int m = (wm + 32 * i) / WI + 2 * v + 4 * g;
-                float out[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) out[q] = SILU ? silu_mul(acc[i][j][v + q], acc[i + WI - 1][j][v + q]) : acc[i][j][v + q];
-                if (m < outs) put4(row + m, out, outs - m, p.vec);
-            }
-        }
+        for (int i = 0; i + 1 < D; ++i) ahead[i] = ahead[i + 1];
+        --waiting;
     }
 }
 

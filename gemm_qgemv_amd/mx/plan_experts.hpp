@@ -26,13 +26,6 @@ struct SortParams {
     int32_t *offsets, *order, *slots;
 };
 
-// The wave's LDS accesses before this come before those after it.
-__device__ __forceinline__ void wave_order()
-{
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // An expert's number, or `experts` for a pair that belongs to none.
 __device__ __forceinline__ int sort_key(const SortParams &p, int64_t pair)
 {

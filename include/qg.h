@@ -520,7 +520,7 @@ typedef enum {
 } qmx_act;
 
 #define QMX_MAX_K (1 << 21)
-#define QMX_MAX_M (1 << 24)
+#define QMX_MAX_M (1 << 23)
 #define QMOE_MAX_EXPERTS 1024
 #define QMOE_MAX_TOP 32
 
@@ -565,10 +565,10 @@ int qmx_dequant(int fmt, const void *codes, const void *scales, int64_t rows, in
  * to call; the rounding of a row depends on how many rows there are.
  *   xfmt   QMX_E2M1 or QMX_E4M3;  W is QMX_E2M1
  *   y      `dtype` [N][M], 16-byte aligned
- *   1 <= M <= QMX_MAX_M, 0 <= N <= 2^31 - 1, the tiles of a launch below 2^24
- *   (QG_ERR_SHAPE).
- * Workspace: qmx_gemm_workspace_bytes(...) for the same arguments (partial
- * sums where few rows leave too few tiles and K is split).
+ *   1 <= M <= QMX_MAX_M, 0 <= N <= 2^31 - 1, the workgroups and tiles of a
+ *   launch below 2^24 (QG_ERR_SHAPE).
+ * Workspace: qmx_gemm_workspace_bytes(...) for the same arguments (both
+ * operands' scales in the order in which tiles of many rows take them).
  */
 int qmx_gemm(int xfmt, const void *x_codes, const void *x_scales, const void *w_codes,
              const void *w_scales, int act, int dtype, void *y, int64_t M, int64_t K, int64_t N,
