@@ -149,7 +149,7 @@ __global__ __launch_bounds__(kFewThreads) void mx_few_kernel(MxGemmParams p)
 #pragma unroll
             for (int w = 0; w < kFewWaves; ++w) v[i] += reinterpret_cast<const float *>(&sums[w][i * NJ + j][at])[m & 3];
         }
-        const float out = SILU ? silu_mul(v[0], v[WI - 1]) : v[0];
+        const float out = !SILU ? v[0] : sizeof(T) == 4 ? silu_mul(v[0], v[WI - 1]) : silu_mul_bf16(v[0], v[WI - 1]);
         if (m < outs && 16 * j + n < rows) {
             T *dst = static_cast<T *>(p.y) + (r0 + 16 * j + n) * p.M + m0 + m;
             if constexpr (sizeof(T) == 4)

@@ -38,13 +38,17 @@ void launch_few(const Call &c, qg::MxGemmParams p, hipStream_t stream)
 int64_t weight_rows(const Call &c) { return c.M * (c.act == QMX_SILU_MUL ? 2 : 1) * (c.grouped ? c.experts : 1); }
 int64_t scale_stages(const Call &c) { return ceil_div(c.K, qg::kTileK); }
 size_t weight_scale_bytes(const Call &c) { return align256(static_cast<size_t>(scale_stages(c)) * weight_rows(c) * qg::kTileScale); }
-size_t tile_workspace(const Call &c)
+size_t row_scale_bytes(const Call &c) { return align256(static_cast<size_t>(scale_stages(c)) * c.N * qg::kTileScale); }
+size_t tile_workspace(const Call &c, int64_t bn)
 {
-    return weight_scale_bytes(c) + align256(static_cast<size_t>(scale_stages(c)) * c.N * qg::kTileScale);
+    return weight_scale_bytes(c) + row_scale_bytes(c) + (c.grouped ? align256(row_tiles(c, bn) * sizeof(qg::MxTileEntry)) : 0);
 }
-int64_t scale_workgroups(const Call &c) { return ceil_div(weight_rows(c), 64) + ceil_div(c.N, 64); }
+int64_t scale_workgroups(const Call &c, int64_t bn)
+{
+    return ceil_div(weight_rows(c), 64) + ceil_div(c.N, 64) + (c.grouped ? ceil_div(row_tiles(c, bn), qg::kScaleThreads) : 0);
+}
 
-void launch_scales(const Call &c, qg::MxGemmParams &p, void *ws, hipStream_t stream)
+void launch_scales(const Call &c, int bn, qg::MxGemmParams &p, void *ws, hipStream_t stream)
 {
     qg::MxScalesParams s{};
     s.ws = p.ws;
@@ -60,7 +64,14 @@ void launch_scales(const Call &c, qg::MxGemmParams &p, void *ws, hipStream_t str
     s.order = p.order;
     s.x_rows = p.x_rows;
     s.top = p.top;
-    hipLaunchKernelGGL(qg::mx_scales_kernel, dim3(static_cast<unsigned>(scale_workgroups(c))), dim3(qg::kScaleThreads), 0, stream, s);
+    s.xblocks = static_cast<int32_t>(ceil_div(c.N, 64));
+    s.offsets = p.offsets;
+    s.experts = p.experts;
+    s.tiles_n = static_cast<int32_t>(row_tiles(c, bn));
+    s.bn = bn;
+    s.tiles = reinterpret_cast<qg::MxTileEntry *>(s.to_x + row_scale_bytes(c));
+    p.tiles = s.tiles;
+    hipLaunchKernelGGL(qg::mx_scales_kernel, dim3(static_cast<unsigned>(scale_workgroups(c, bn))), dim3(qg::kScaleThreads), 0, stream, s);
     p.ws = s.to_w;
     p.xs = s.to_x;
     p.ws_rows = s.wrows;
@@ -69,7 +80,7 @@ void launch_scales(const Call &c, qg::MxGemmParams &p, void *ws, hipStream_t str
 template <int XF, typename T, bool SILU, bool GROUPED, int BM, int BN, int WM, int WN, int D>
 void launch_tile(const Call &c, qg::MxGemmParams p, void *ws, hipStream_t stream)
 {
-    launch_scales(c, p, ws, stream);
+    launch_scales(c, BN, p, ws, stream);
     p.tiles_m = static_cast<int>(ceil_div(c.M, BM / (SILU ? 2 : 1)));
     p.tiles_n = static_cast<int>(row_tiles(c, BN));
     static std::atomic<uint64_t> asked{0};
@@ -97,14 +108,25 @@ Kind choose(const Call &c)
     return kTile64;
 }
 
-size_t workspace(const Call &c) { return c.N == 0 || choose(c) == kFew16 ? 0 : tile_workspace(c); }
+// Rows of x that a tile holds.
+int64_t tile_rows(const Call &c)
+{
+    switch (choose(c)) {
+        case kFew16: return 16;
+        case kTile64: return 64;
+        case kTile128: return 128;
+        default: return c.xfmt == QMX_E2M1 && c.act == QMX_NONE && !c.grouped ? 256 : 128;
+    }
+}
+
+size_t workspace(const Call &c) { return c.N == 0 || choose(c) == kFew16 ? 0 : tile_workspace(c, tile_rows(c)); }
 
 // Workgroups of the call's launches, and tiles (more than a launch takes are refused).
 int64_t workgroups(const Call &c)
 {
     const int64_t wide = c.M * (c.act == QMX_SILU_MUL ? 2 : 1);
     if (choose(c) == kFew16) return ceil_div(c.M, 16) * row_tiles(c, 16);
-    return std::max(scale_workgroups(c), ceil_div(wide, 64) * row_tiles(c, 64));
+    return std::max(scale_workgroups(c, 64), ceil_div(wide, 64) * row_tiles(c, 64));
 }
 
 template <int XF, typename T, bool SILU, bool GROUPED>
@@ -120,7 +142,7 @@ void launch(const Call &c, const qg::MxGemmParams &p, void *ws, hipStream_t stre
             else if constexpr (XF == qg::kMxE2M1)
                 return launch_tile<XF, T, SILU, GROUPED, 256, 128, 4, 2, 3>(c, p, ws, stream);
             else
-                return launch_tile<XF, T, SILU, GROUPED, 256, 128, 4, 2, 2>(c, p, ws, stream);
+                return launch_tile<XF, T, SILU, GROUPED, 256, 128, 2, 4, 2>(c, p, ws, stream);
     }
 }
 

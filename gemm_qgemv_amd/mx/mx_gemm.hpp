@@ -37,6 +37,8 @@ namespace qg {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
+struct MxTileEntry;
+
 struct MxGemmParams {
     const uint8_t *xc, *xs, *wc, *ws;
     void *y;
@@ -44,7 +46,10 @@ struct MxGemmParams {
     int64_t N;               // rows (grouped: pairs)
     int32_t K, pitch;        // inputs a row, bytes of a row of scales
     int32_t tiles_m, tiles_n;
-    int64_t ws_rows;         // tiles: rows of the weights' scales, which are laid out for them, as x's are
+    // tiles only (mx_tile.hpp): rows of the weights' scales, which are laid out for
+    // them as x's are, and the grouped form's list of tiles
+    int64_t ws_rows;
+    const MxTileEntry *tiles;
     // grouped only
     const int32_t *offsets;  // [experts + 1]
     const int32_t *order;    // pair of each sorted row, or NULL: x lies sorted
@@ -54,11 +59,12 @@ struct MxGemmParams {
 };
 
 // Four e4m3 numbers as those of at least 4 in size (NaN too) and the others,
-// zeros in the others' places: 4 is code 0x48.
+// zeros in the others' places: 4 is code 0x48, and v_perm_b32 makes a byte of ones
+// or zeros of the top bit of bytes 1 and 3 of either operand (selectors 8..11).
 __device__ __forceinline__ void e4m3_parts(uint32_t x, int &large, int &small)
 {
-    const uint32_t top = ((x & 0x7f7f7f7fu) + 0x38383838u) & 0x80808080u;
-    const uint32_t mask = top | (top - (top >> 7));
+    const uint32_t top = (x & 0x7f7f7f7fu) + 0x38383838u;
+    const uint32_t mask = __builtin_amdgcn_perm(top, top << 8, 0x0b090a08u);
     large = static_cast<int>(x & mask);
     small = static_cast<int>(x & ~mask);
 }
@@ -145,6 +151,15 @@ __device__ __forceinline__ int64_t x_row(const MxGemmParams &p, int64_t r0, int 
     if (pair < 0 || pair >= p.N) return -1;
     const int64_t row = static_cast<uint32_t>(pair) / p.top;
     return row < p.x_rows ? row : -1;
+}
+
+// g / (1 + exp(-g)) * u for outputs that are rounded to bf16 next: the exponential's
+// argument is rounded to float32, so the result is off by up to |g| 2^-23 of
+// it, 2^-17 of it where it is largest (against 2^-9), in a third of the instructions.
+__device__ __forceinline__ float silu_mul_bf16(float g, float u)
+{
+    const float t = __builtin_amdgcn_exp2f(g * -0x1.715476p+0f);
+    return g * __builtin_amdgcn_rcpf(1.0f + t) * u;
 }
 
 // g / (1 + exp(-g)) * u. With t = exp(-|g|), which does not overflow, the factor is

@@ -134,7 +134,7 @@ __device__ __forceinline__ void mx_tile_store(const f32x16 (&acc)[TI][TJ], T *y,
             __builtin_amdgcn_sched_barrier(0);
             float out[16];
 #pragma unroll
-            for (int v = 0; v < 16; ++v) out[v] = SILU ? silu_mul(acc[i][j][v], acc[i + WI - 1][j][v]) : acc[i][j][v];
+            for (int v = 0; v < 16; ++v) out[v] = !SILU ? acc[i][j][v] : SIZE == 4 ? silu_mul(acc[i][j][v], acc[i + WI - 1][j][v]) : silu_mul_bf16(acc[i][j][v], acc[i + WI - 1][j][v]);
             if constexpr (SIZE == 4) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -193,6 +193,16 @@ struct MxScalesParams {
     const int32_t *order;
     int64_t x_rows;           // rows that may be gathered
     FastDiv top;
+    // grouped: the list of tiles of BN rows
+    int32_t xblocks;          // workgroups that take x's rows; those behind list tiles
+    const int32_t *offsets;
+    int32_t experts, tiles_n, bn;
+    MxTileEntry *tiles;
+};
+
+// A tile of rows: rows r0 .. r0 + rows - 1 of expert e; rows 0: none.
+struct MxTileEntry {
+    int32_t e, r0, rows, pad;
 };
 
 constexpr int kScaleThreads = 256;
@@ -220,12 +230,59 @@ __device__ __forceinline__ void mx_scales_rows(const MxScalesParams &p, const ui
     }
 }
 
+// Every expert's rows in tiles, expert by expert: a thread finds one tile's expert
+// in the running sums of tiles (offsets out of range are cut, so that any
+// contents give rows in [0, pairs)).
+__device__ __forceinline__ void mx_list_tiles(const MxScalesParams &p, int first)
+{
+    __shared__ int upto[kMaxExperts];                // tiles of the experts up to each
+    __shared__ int waves[kScaleThreads / 64];
+    constexpr int C = kMaxExperts / kScaleThreads;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, most = static_cast<int>(p.xrows);
+    const auto place = [&](int e) { return max(0, min(p.offsets[min(e, p.experts)], most)); };
+    int o[C + 1], mine = 0;
+#pragma unroll
+    for (int j = 0; j <= C; ++j) o[j] = place(threadIdx.x * C + j);
+#pragma unroll
+    for (int j = 0; j < C; ++j) mine += (max(o[j + 1] - o[j], 0) + p.bn - 1) / p.bn;
+    int sum = wave_inclusive_sum32(mine);
+    if (lane == 63) waves[wave] = sum;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) sum += waves[w];
+    sum -= mine;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        sum += (max(o[j + 1] - o[j], 0) + p.bn - 1) / p.bn;
+        upto[threadIdx.x * C + j] = sum;
+    }
+    __syncthreads();
+    const int tile = first + threadIdx.x;
+    if (tile >= p.tiles_n) return;
+    int lo = 0, hi = kMaxExperts;                    // the first expert with more tiles up to it
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (upto[mid] > tile) hi = mid;
+        else lo = mid + 1;
+    }
+    MxTileEntry t{0, 0, 0, 0};
+    if (lo < p.experts) {
+        const int begin = place(lo), end = place(lo + 1);
+        t.e = lo;
+        t.r0 = begin + (tile - (lo ? upto[lo - 1] : 0)) * p.bn;
+        t.rows = min(p.bn, end - t.r0);
+    }
+    p.tiles[tile] = t;
+}
+
 static __global__ __launch_bounds__(kScaleThreads) void mx_scales_kernel(MxScalesParams p)
 {
-    if (static_cast<int>(blockIdx.x) < p.wblocks)
-        mx_scales_rows(p, p.ws, p.to_w, p.wrows, int64_t(blockIdx.x) * 64, false);
+    const int block = blockIdx.x;
+    if (block < p.wblocks)
+        mx_scales_rows(p, p.ws, p.to_w, p.wrows, int64_t(block) * 64, false);
+    else if (block < p.wblocks + p.xblocks)
+        mx_scales_rows(p, p.xs, p.to_x, p.xrows, int64_t(block - p.wblocks) * 64, p.order != nullptr);
     else
-        mx_scales_rows(p, p.xs, p.to_x, p.xrows, int64_t(blockIdx.x - p.wblocks) * 64, p.order != nullptr);
+        mx_list_tiles(p, (block - p.wblocks - p.xblocks) * kScaleThreads);
 }
 
 template <int XF, typename T, bool SILU, bool GROUPED, int BM, int BN, int WM, int WN, int D>
@@ -260,9 +317,9 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
             const int tm = in / high, tn = band * BAND + in % high;
             t.m0 = tm * OUTS;
             if constexpr (GROUPED) {
-                const GroupTile u = group_tile<BN>(p.offsets, p.experts, p.N, tn);
-                if (u.e < 0) continue;
-                t.e = u.e, t.r0 = u.r0, t.rows = u.r1 - u.r0;
+                const MxTileEntry u = p.tiles[tn];
+                if (u.rows == 0) continue;
+                t.e = u.e, t.r0 = u.r0, t.rows = u.rows;
             } else {
                 t.r0 = tn * BN;
                 t.rows = static_cast<int>(min(int64_t(BN), p.N - t.r0));
@@ -293,6 +350,16 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
     const uint8_t *sbase;
     int64_t srows;           // rows of a stage
     int slen;
+    // grouped: of a tile's rows that this wave loads, one a lane, the pair (asked for
+    // a stage before the tile is opened)
+    const auto table_row = [&](int lane) { return XR * (lane / XR * NW + wave) + lane % XR; };
+    int64_t pair = -1;
+    const auto ask = [&](const MxTile &t) {
+        if constexpr (GROUPED) {
+            const int lane = mx_here(threadIdx.x & 63), row = table_row(lane);
+            if (p.order && lane < BN / NW && row < t.rows) pair = p.order[int64_t(t.r0) + row];
+        }
+    };
     const auto open = [&](const MxTile &t) {
         const int lane = mx_here(threadIdx.x & 63);
         at = 0;
@@ -311,10 +378,13 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
         if constexpr (GROUPED) {
             // where the rows that this wave's loads take begin, one a lane, kept in LDS for all of the tile's stages
             static_assert(BN / NW <= 64, "a lane a row");
-            if (lane < BN / NW) {
-                const int64_t x = x_row<true>(p, t.r0, t.rows, XR * (lane / XR * NW + wave) + lane % XR);
-                row_table[lane] = x < 0 ? kMxOut : static_cast<uint32_t>(x * xrb);
+            const int row = table_row(lane);
+            int64_t x = row;
+            if (p.order) {
+                x = static_cast<uint32_t>(pair) / p.top;
+                if (pair < 0 || pair >= p.N || x >= p.x_rows) x = -1;
             }
+            if (lane < BN / NW) row_table[lane] = x < 0 || row >= t.rows ? kMxOut : static_cast<uint32_t>(x * xrb);
             wave_order();
         }
     };
@@ -361,24 +431,29 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
         ops[0].read(src + wm * L::wrow, src + L::x + wn * L::xrow, 0, r, g);
     };
 
-    // tiles that are loaded, at least in part, behind the current one
-    MxTile cur = next_tile(), ahead[D];
+    // tiles that are loaded, at least in part, behind the current one, and the one after
+    MxTile cur = next_tile(), ahead[D], after{0, 0, 0, 0};
     if (cur.rows == 0) return;
     int waiting = 0;
     bool more = true;
+    ask(cur);
     open(cur);
-    // takes the next stage's tile
+    // takes the next stage's tile; looks for the tile after at its last stage
     const auto advance = [&]() {
-        if (more && at == stages) {
-            const MxTile t = next_tile();
-            more = t.rows != 0;
+        if (!more) return;
+        if (at == stages) {
+            more = after.rows != 0;
             if (more) {
-                open(t);
+                open(after);
 #pragma unroll
                 for (int i = 0; i < D; ++i)
-                    if (i == waiting) ahead[i] = t;
+                    if (i == waiting) ahead[i] = after;
                 ++waiting;
             }
+        }
+        if (at == stages - 1) {
+            after = next_tile();
+            ask(after);
         }
     };
     for (int d = 0; d < D; ++d) {
