@@ -25,12 +25,12 @@ int64_t row_tiles(const Call &c, int64_t T)
     return std::min(c.N, (c.N + some * (T - 1)) / T);
 }
 
-template <int XF, typename T, bool SILU, bool GROUPED, int NJ>
+template <int XF, typename T, bool SILU, bool GROUPED, int MI, int KS>
 void launch_few(const Call &c, qg::MxGemmParams p, hipStream_t stream)
 {
-    p.tiles_m = static_cast<int>(ceil_div(c.M, 16));
-    p.tiles_n = static_cast<int>(row_tiles(c, 16 * NJ));
-    hipLaunchKernelGGL((qg::mx_few_kernel<XF, T, SILU, GROUPED, NJ>), dim3(static_cast<unsigned>(int64_t(p.tiles_m) * p.tiles_n)),
+    p.tiles_m = static_cast<int>(ceil_div(c.M, 16 * MI * qg::kFewWaves / KS));
+    p.tiles_n = static_cast<int>(row_tiles(c, 16));
+    hipLaunchKernelGGL((qg::mx_few_kernel<XF, T, SILU, GROUPED, MI, KS>), dim3(static_cast<unsigned>(int64_t(p.tiles_m) * p.tiles_n)),
                        dim3(qg::kFewThreads), 0, stream, p);
 }
 
@@ -133,7 +133,11 @@ template <int XF, typename T, bool SILU, bool GROUPED>
 void launch(const Call &c, const qg::MxGemmParams &p, void *ws, hipStream_t stream)
 {
     switch (choose(c)) {
-        case kFew16: return launch_few<XF, T, SILU, GROUPED, 1>(c, p, stream);
+        case kFew16:
+            // waves side by side where there are enough of them, else four to an output block
+            if (ceil_div(c.M, 32) * row_tiles(c, 16) >= 4 * kComputeUnits)
+                return launch_few<XF, T, SILU, GROUPED, SILU ? 1 : 2, 1>(c, p, stream);
+            return launch_few<XF, T, SILU, GROUPED, 1, 4>(c, p, stream);
         case kTile64: return launch_tile<XF, T, SILU, GROUPED, 64, 64, 1, 2, 2>(c, p, ws, stream);
         case kTile128: return launch_tile<XF, T, SILU, GROUPED, 128, 128, 2, 2, 2>(c, p, ws, stream);
         default:
