@@ -18,6 +18,7 @@ ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", "qg.hip"), os.path.join(HERE, "serve", "kv.hip"),
            os.path.join(HERE, "serve", "attn.hip"), os.path.join(HERE, "serve", "logprobs.hip"),
            os.path.join(HERE, "mx", "quant.hip"), os.path.join(HERE, "mx", "mx_gemm.hip"),
+           os.path.join(HERE, "mx", "mx_few.hip"), os.path.join(HERE, "mx", "mx_mid.hip"), os.path.join(HERE, "mx", "mx_tile.hip"),
            os.path.join(HERE, "mx", "moe.hip")]
 OUT = os.path.join(HERE, "libqg.so")
 PROBE_SRC = os.path.join(HERE, "csrc", "probe.hip")
