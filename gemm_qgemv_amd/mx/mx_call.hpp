@@ -56,7 +56,11 @@ void mx_dispatch(const MxCall &c, F f)
 }
 
 // The launches of each kernel's file.
-void mx_launch_few(const MxCall &c, const MxGemmParams &p, bool side_by_side, hipStream_t stream);
+// blocks: of 16 outputs a wave takes (1 with SILU), waves: that split K
+void mx_launch_few(const MxCall &c, const MxGemmParams &p, int blocks, int waves, hipStream_t stream);
+// mi: blocks of 16 weight rows a wave takes (2 or 4), nj: blocks of 16 rows of x (2, 4,
+// and 6, or where mi is 4 mx_mid_most: more would not fit in registers)
+constexpr int mx_mid_most(int xfmt) { return xfmt == QMX_E2M1 ? 6 : 5; }
 void mx_launch_mid(const MxCall &c, const MxGemmParams &p, int mi, int nj, hipStream_t stream);
 // size: 64, 128 or 256, the tile's weight rows
 void mx_launch_tile(const MxCall &c, const MxGemmParams &p, int size, void *ws, hipStream_t stream);

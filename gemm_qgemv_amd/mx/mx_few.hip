@@ -4,7 +4,7 @@
 
 namespace qg {
 
-void mx_launch_few(const MxCall &c, const MxGemmParams &from, bool side_by_side, hipStream_t stream)
+void mx_launch_few(const MxCall &c, const MxGemmParams &from, int blocks, int waves, hipStream_t stream)
 {
     const auto go = [&](auto kernel, int outputs) {
         MxGemmParams p = from;
@@ -14,11 +14,19 @@ void mx_launch_few(const MxCall &c, const MxGemmParams &from, bool side_by_side,
     };
     mx_dispatch(c, [&](auto form) {
         using F = decltype(form);
-        constexpr int MI = F::SILU ? 1 : 2;
-        if (side_by_side)
-            go(mx_few_kernel<F::XF, typename F::T, F::SILU, F::GROUPED, MI, 1>, 16 * MI * kFewWaves);
+        const auto split = [&](auto mi) {
+            constexpr int MI = decltype(mi)::value, EACH = 16 * MI * kFewWaves;
+            if (waves == 4)
+                go(mx_few_kernel<F::XF, typename F::T, F::SILU, F::GROUPED, MI, 4>, EACH / 4);
+            else if (waves == 2)
+                go(mx_few_kernel<F::XF, typename F::T, F::SILU, F::GROUPED, MI, 2>, EACH / 2);
+            else
+                go(mx_few_kernel<F::XF, typename F::T, F::SILU, F::GROUPED, MI, 1>, EACH);
+        };
+        if constexpr (F::SILU)
+            split(std::integral_constant<int, 1>{});
         else
-            go(mx_few_kernel<F::XF, typename F::T, F::SILU, F::GROUPED, 1, kFewWaves>, 16);
+            blocks == 2 ? split(std::integral_constant<int, 2>{}) : split(std::integral_constant<int, 1>{});
     });
 }
 

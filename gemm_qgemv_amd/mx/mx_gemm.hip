@@ -9,22 +9,41 @@ using Call = qg::MxCall;
 // Which kernel a call takes.
 struct Choice {
     enum Kind { kFew, kMid, kTile } kind;
-    int size;        // kFew: waves side by side or not; kMid: blocks of weight rows; kTile: weight rows
-    int blocks;      // kMid: blocks of 16 rows
+    int size;        // kFew, kMid: blocks of 16 weight rows a wave takes (kFew: of outputs); kTile: weight rows
+    int blocks;      // kFew: waves that split K; kMid: blocks of 16 rows
 };
 
 // Rows that a tile has to fill: of an expert on average in the grouped form.
 int64_t usual_rows(const Call &c) { return c.grouped ? ceil_div(c.N, c.experts) : c.N; }
 
+// Measured, e4m3 rows (e2m1 in brackets), outputs x K x rows:
+//  few against mid     2048 x 8192 x 24: 10 against 19 us [7.6, 17]; 6144 x 2048 x 60:
+//                      12, 11 [9, 8]; 17408 x 5120 x 24: 32, 21 [22, 18]
+//  few against tiles   1024 x 2048 x 256: 9, 17.5 [7.5, 12]; 2048 x 8192 x 200: 45, 51 [33, 29]
+//  mid against tiles   17408 x 5120 x 60: 34, 45 [21, 27]; x 90: 45, 45 [24, 28]
+//  mid of 64 weight rows a wave pair against 128   6144 x 2048 x 60: 11, 15 [8, 11];
+//                      17408 x 5120 x 77: 45, 37 [27, 22]
 Choice choose(const Call &c)
 {
-    const int64_t rows = usual_rows(c);
-    if (rows <= 16) return {Choice::kFew, ceil_div(c.M, 32) * c.row_tiles(16) >= 4 * kComputeUnits, 0};
-    if (rows <= 128) {
-        const int nj = rows <= 32 ? 2 : rows <= 64 ? 4 : rows <= 96 ? 6 : 8;
-        return {Choice::kMid, ceil_div(c.wide(), 128) * c.row_tiles(16 * nj) >= kComputeUnits ? 4 : 2, nj};
+    const int64_t rows = usual_rows(c), wide = c.wide();
+    // Workgroups of 16 outputs x 16 rows whose waves split K: for 16 rows, and
+    // wherever they are few, since larger ones would leave compute units idle (the
+    // weights that several read come from the caches).
+    if (rows <= 16 || ceil_div(wide, 16) * c.row_tiles(16) <= 4 * kComputeUnits) {
+        // as many waves share outputs as have a run of inputs each; two blocks of
+        // outputs a wave once every compute unit gets a workgroup of four such waves
+        const int64_t runs = ceil_div(c.K, 512);
+        return {Choice::kFew, c.act == QMX_NONE && ceil_div(c.M, 32) * c.row_tiles(16) >= kComputeUnits ? 2 : 1, runs > 2 ? 4 : runs > 1 ? 2 : 1};
     }
-    const auto tiles = [&](int size) { return ceil_div(c.wide(), size) * c.row_tiles(qg::mx_tile_rows(c, size)); };
+    // The weights straight to registers, while x's rows are one tile: 128 weight rows a
+    // workgroup once those of 64 are more than the compute units.
+    if (rows <= 96) {
+        const int nj = rows <= 32 ? 2 : rows <= 64 ? 4 : 6;
+        if (ceil_div(wide, 64) * c.row_tiles(16 * nj) <= kComputeUnits) return {Choice::kMid, 2, nj};
+        const int most = qg::mx_mid_most(c.xfmt);
+        if (rows <= 16 * most) return {Choice::kMid, 4, std::min(nj, most)};
+    }
+    const auto tiles = [&](int size) { return ceil_div(wide, size) * c.row_tiles(qg::mx_tile_rows(c, size)); };
     if (tiles(256) >= 2 * kComputeUnits) return {Choice::kTile, 256, 0};
     if (tiles(128) >= kComputeUnits) return {Choice::kTile, 128, 0};
     return {Choice::kTile, 64, 0};
@@ -41,7 +60,7 @@ size_t workspace(const Call &c)
 int64_t workgroups(const Call &c)
 {
     const Choice k = choose(c);
-    if (k.kind == Choice::kFew) return ceil_div(c.M, 16) * c.row_tiles(16);
+    if (k.kind == Choice::kFew) return ceil_div(c.M, 64 * k.size / k.blocks) * c.row_tiles(16);
     if (k.kind == Choice::kMid) return ceil_div(c.wide(), 32 * k.size) * c.row_tiles(16 * k.blocks);
     return qg::mx_tile_workgroups(c, k.size);
 }
@@ -50,7 +69,7 @@ void launch(const Call &c, const qg::MxGemmParams &p, void *ws, hipStream_t stre
 {
     const Choice k = choose(c);
     switch (k.kind) {
-        case Choice::kFew: return qg::mx_launch_few(c, p, k.size != 0, stream);
+        case Choice::kFew: return qg::mx_launch_few(c, p, k.size, k.blocks, stream);
         case Choice::kMid: return qg::mx_launch_mid(c, p, k.size, k.blocks, stream);
         default: return qg::mx_launch_tile(c, p, k.size, ws, stream);
     }

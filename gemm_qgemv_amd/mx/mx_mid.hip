@@ -24,16 +24,12 @@ void mx_launch_mid(const MxCall &c, const MxGemmParams &p, int mi, int nj, hipSt
 {
     mx_dispatch(c, [&](auto form) {
         using F = decltype(form);
-        const auto rows = [&](auto blocks) {
-            constexpr int MI = decltype(blocks)::value;
-            switch (nj) {
-                case 2: return launch<F, MI, 2>(c, p, stream);
-                case 4: return launch<F, MI, 4>(c, p, stream);
-                case 6: return launch<F, MI, 6>(c, p, stream);
-                default: return launch<F, MI, 8>(c, p, stream);
-            }
-        };
-        mi == 4 ? rows(std::integral_constant<int, 4>{}) : rows(std::integral_constant<int, 2>{});
+        constexpr int most = mx_mid_most(F::XF == kMxE2M1 ? QMX_E2M1 : QMX_E4M3);
+        switch (nj) {
+            case 2: return mi == 4 ? launch<F, 4, 2>(c, p, stream) : launch<F, 2, 2>(c, p, stream);
+            case 4: return mi == 4 ? launch<F, 4, 4>(c, p, stream) : launch<F, 2, 4>(c, p, stream);
+            default: return mi == 4 ? launch<F, 4, most>(c, p, stream) : launch<F, 2, 6>(c, p, stream);
+        }
     });
 }
 

@@ -40,7 +40,9 @@ struct MxTileLds {
 template <int CHUNKS>
 __device__ __forceinline__ int mx_swizzle(int r)
 {
-    return CHUNKS == 16 ? r & 15 : (r & 7) ^ ((r >> 3) & 1);
+    if constexpr (CHUNKS == 16) return r & 15;
+    if constexpr (CHUNKS == 8) return (r & 7) ^ ((r >> 3) & 1);
+    return (((r >> 1) ^ (r >> 2)) & 1) | ((((r >> 2) ^ (r >> 3)) & 1) << 1);
 }
 
 // The operands of one step (64 inputs) of a wave, from LDS (wl and xl: its first rows).
