@@ -268,10 +268,13 @@ __device__ __forceinline__ void mx_list_tiles(const MxScalesParams &p, int first
     }
     MxTileEntry t{0, 0, 0, 0};
     if (lo < p.experts) {
-        const int begin = place(lo), end = place(lo + 1);
-        t.e = lo;
-        t.r0 = begin + (tile - (lo ? upto[lo - 1] : 0)) * p.bn;
-        t.rows = min(p.bn, end - t.r0);
+        const int begin = place(lo), rows = max(place(lo + 1) - begin, 0), nth = tile - (lo ? upto[lo - 1] : 0);
+        // (no plan's offsets may make the sums run over)
+        if (nth >= 0 && nth < (rows + p.bn - 1) / p.bn) {
+            t.e = lo;
+            t.r0 = begin + nth * p.bn;
+            t.rows = min(p.bn, rows - nth * p.bn);
+        }
     }
     p.tiles[tile] = t;
 }
