@@ -50,6 +50,7 @@ struct MxGemmParams {
     // them as x's are, and the grouped form's list of tiles
     int64_t ws_rows;
     const MxTileEntry *tiles;
+    const uint32_t *x_at;    // where a sorted row's codes begin, with `order`
     // grouped only
     const int32_t *offsets;  // [experts + 1]
     const int32_t *order;    // pair of each sorted row, or NULL: x lies sorted

@@ -11,6 +11,8 @@ int64_t weight_rows(const MxCall &c) { return c.wide() * (c.grouped ? c.experts 
 int64_t scale_stages(const MxCall &c) { return ceil_div(c.K, kTileK); }
 size_t weight_scale_bytes(const MxCall &c) { return align256(static_cast<size_t>(scale_stages(c)) * weight_rows(c) * kTileScale); }
 size_t row_scale_bytes(const MxCall &c) { return align256(static_cast<size_t>(scale_stages(c)) * c.N * kTileScale); }
+// grouped: the list of tiles, and behind it where the sorted rows' codes begin
+int64_t tile_list(const MxCall &c, int64_t bn) { return static_cast<int64_t>(align256(c.row_tiles(bn) * sizeof(MxTileEntry)) / sizeof(MxTileEntry)); }
 int64_t scale_workgroups(const MxCall &c, int64_t bn)
 {
     return ceil_div(weight_rows(c), 64) + ceil_div(c.N, 64) + (c.grouped ? ceil_div(c.row_tiles(bn), kScaleThreads) : 0);
@@ -39,6 +41,9 @@ void launch_scales(const MxCall &c, int bn, MxGemmParams &p, void *ws, hipStream
     s.bn = bn;
     s.tiles = reinterpret_cast<MxTileEntry *>(s.to_x + row_scale_bytes(c));
     p.tiles = s.tiles;
+    s.x_at = reinterpret_cast<uint32_t *>(s.tiles + (c.grouped ? tile_list(c, bn) : 0));
+    s.xrb = static_cast<int32_t>(mx_row_bytes(c.xfmt, c.K));
+    p.x_at = s.x_at;
     hipLaunchKernelGGL(mx_scales_kernel, dim3(static_cast<unsigned>(scale_workgroups(c, bn))), dim3(kScaleThreads), 0, stream, s);
     p.ws = s.to_w;
     p.xs = s.to_x;
@@ -52,7 +57,7 @@ void launch(const MxCall &c, MxGemmParams p, void *ws, hipStream_t stream)
     p.tiles_m = static_cast<int>(ceil_div(c.M, BM / (F::SILU ? 2 : 1)));
     p.tiles_n = static_cast<int>(c.row_tiles(BN));
     static std::atomic<uint64_t> asked{0};
-    constexpr size_t bytes = MxTileLds<F::XF, BM, BN, WM * WN, D>::bytes;
+    constexpr size_t bytes = MxTileLds<F::XF, F::GROUPED, BM, BN, WM * WN, D>::bytes;
     constexpr int64_t per = 160 * 1024 / bytes;      // workgroups that a compute unit holds
     static_assert(per >= 1, "LDS of a compute unit");
     const auto kernel = &mx_tile_kernel<F::XF, typename F::T, F::SILU, F::GROUPED, BM, BN, WM, WN, D>;
@@ -71,7 +76,7 @@ int64_t mx_tile_rows(const MxCall &c, int size)
 size_t mx_tile_workspace(const MxCall &c, int size)
 {
     return weight_scale_bytes(c) + row_scale_bytes(c) +
-           (c.grouped ? align256(c.row_tiles(mx_tile_rows(c, size)) * sizeof(MxTileEntry)) : 0);
+           (c.grouped ? tile_list(c, mx_tile_rows(c, size)) * sizeof(MxTileEntry) + align256(c.N * 4) : 0);
 }
 
 int64_t mx_tile_workgroups(const MxCall &c, int size)

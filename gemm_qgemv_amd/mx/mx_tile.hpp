@@ -19,6 +19,8 @@
 // in turn, so that a lane holds both numbers of an output.
 #pragma once
 
+#include <type_traits>
+
 #include "mx_gemm.hpp"
 
 namespace qg {
@@ -26,13 +28,13 @@ namespace qg {
 constexpr int kTileK = 256;      // inputs of a stage
 constexpr int kTileScale = kTileK / kMxBlock;      // bytes of scales of a row and stage
 
-template <int XF, int BM, int BN, int NW, int D>
+template <int XF, bool GROUPED, int BM, int BN, int NW, int D>
 struct MxTileLds {
     static constexpr int wrow = kTileK / 2, xrow = static_cast<int>(mx_bytes<XF>(kTileK));
     static constexpr int wb = (BM + 127) / 128, xb = (BN + 127) / 128;    // loads of scales: 128 rows, 1 KiB
     static constexpr int x = BM * wrow, sw = x + BN * xrow, sx = sw + wb * 1024, stage = sx + xb * 1024;
-    static constexpr int table = D * stage;                               // grouped: the rows of x behind a tile's
-    static constexpr int bytes = table + BN * 4;
+    static constexpr int table = D * stage, tables = GROUPED ? NW * 256 : 0;      // where rows of x begin, of three tiles
+    static constexpr int bytes = table + 3 * tables + (GROUPED ? 256 : 0);        // (the last for what nobody wants)
 };
 
 // 16-byte chunk c of LDS row r lies at chunk c ^ swizzle(r): 16 lanes that
@@ -194,6 +196,8 @@ struct MxScalesParams {
     int32_t stages;
     const int32_t *order;
     int64_t x_rows;           // rows that may be gathered
+    uint32_t *x_at;           // with `order`: where each row's codes begin, or kMxOut
+    int32_t xrb;              // bytes of a row's codes
     FastDiv top;
     // grouped: the list of tiles of BN rows
     int32_t xblocks;          // workgroups that take x's rows; those behind list tiles
@@ -211,24 +215,26 @@ constexpr int kScaleThreads = 256;
 
 __device__ __forceinline__ void mx_scales_rows(const MxScalesParams &p, const uint8_t *from, uint8_t *to, int64_t rows, int64_t first, bool gather)
 {
-    // lanes along rows: stores side by side; a row's line is read by one lane stage after stage
+    // lanes along rows, so that stores lie side by side; of a row 16 bytes, two stages', at once
     const int64_t row = first + (threadIdx.x & 63);
     if (row >= rows) return;
-    int64_t at = row;
+    int64_t at = threadIdx.x & 63;
     if (gather) {
         const int64_t pair = p.order[row];
         at = pair < 0 || pair >= rows ? -1 : static_cast<uint32_t>(pair) / p.top;
         if (at >= p.x_rows) at = -1;
+        if (threadIdx.x < 64) p.x_at[row] = at < 0 ? kMxOut : static_cast<uint32_t>(at * p.xrb);
     }
-    for (int t = threadIdx.x >> 6; t < p.stages; t += kScaleThreads / 64) {
-        uint32_t v[2];
+    const auto buf = mx_buffer(from + (gather ? 0 : first * p.pitch), (gather ? p.x_rows : min(int64_t(64), rows - first)) * p.pitch);
+    for (int t = threadIdx.x >> 6; 2 * t < p.stages; t += kScaleThreads / 64) {
+        u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(buf, at < 0 ? kMxOut : static_cast<uint32_t>(at * p.pitch + 16 * t), 0, 0));
 #pragma unroll
-        for (int d = 0; d < 2; ++d) {
-            const int b = t * 8 + 4 * d, left = p.blocks - b;
-            v[d] = at >= 0 && left > 0 ? *reinterpret_cast<const uint32_t *>(from + at * p.pitch + b) : 0;
+        for (int d = 0; d < 4; ++d) {
+            const int left = p.blocks - (16 * t + 4 * d);
             if (left < 4) v[d] &= left <= 0 ? 0 : (1u << (8 * left)) - 1;
         }
-        *reinterpret_cast<u32x2 *>(to + (t * rows + row) * 8) = u32x2{v[0], v[1]};
+        *reinterpret_cast<u32x2 *>(to + (2 * t * rows + row) * 8) = u32x2{v[0], v[1]};
+        if (2 * t + 1 < p.stages) *reinterpret_cast<u32x2 *>(to + ((2 * t + 1) * rows + row) * 8) = u32x2{v[2], v[3]};
     }
 }
 
@@ -294,7 +300,7 @@ template <int XF, typename T, bool SILU, bool GROUPED, int BM, int BN, int WM, i
 __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
 {
     constexpr int NW = WM * WN, TI = BM / WM / 32, TJ = BN / WN / 32, WI = SILU ? 2 : 1;
-    using L = MxTileLds<XF, BM, BN, NW, D>;
+    using L = MxTileLds<XF, GROUPED, BM, BN, NW, D>;
     static_assert(TI % WI == 0, "a wave holds gate and up rows of an output");
     constexpr int OUTS = BM / WI;                    // outputs of a tile
     extern __shared__ __align__(16) uint8_t lds[];
@@ -309,27 +315,55 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
     // first: the 32 tiles that an XCD's compute units work on are 8 x 4, 12
     // operands for 33 in a row.
     int nth = blockIdx.x >> 3;
-    const auto next_tile = [&]() {
+    // f(first id of the XCD's run, its end, workgroups of the XCD)
+    const auto run = [&](auto f) {
         const int ntiles = p.tiles_m * p.tiles_n, xcd = blockIdx.x & 7, xcds = min(8, static_cast<int>(gridDim.x));
-        const int run = ntiles / xcds + (xcd < ntiles % xcds), run0 = xcd * (ntiles / xcds) + min(xcd, ntiles % xcds);
+        f(xcd * (ntiles / xcds) + min(xcd, ntiles % xcds), ntiles / xcds + (xcd < ntiles % xcds), (static_cast<int>(gridDim.x) - xcd + 7) >> 3);
+    };
+    constexpr int BAND = 4;
+    const auto place = [&](int id, int &tm, int &tn) {
+        const int band = id / (BAND * p.tiles_m), in = id - band * (BAND * p.tiles_m);
+        const int high = min(BAND, p.tiles_n - band * BAND);
+        tm = in / high, tn = band * BAND + in % high;
+    };
+    // grouped: the workgroup's next 64 tiles, one a lane, and those not taken yet, so that
+    // a new tile asks for nothing in memory while others' loads are under way (these
+    // come in order: the wait for one is a wait for all before it)
+    MxTile mine{0, 0, 0, 0};
+    uint64_t untaken = 0;
+    const auto next_tile = [&]() __attribute__((always_inline)) {
         MxTile t{0, 0, 0, 0};
-        while (nth < run) {
-            constexpr int BAND = 4;
-            const int id = run0 + nth;
-            nth += (gridDim.x - xcd + 7) >> 3;       // workgroups of this XCD
-            const int band = id / (BAND * p.tiles_m), in = id - band * (BAND * p.tiles_m);
-            const int high = min(BAND, p.tiles_n - band * BAND);
-            const int tm = in / high, tn = band * BAND + in % high;
-            t.m0 = tm * OUTS;
-            if constexpr (GROUPED) {
-                const MxTileEntry u = p.tiles[tn];
-                if (u.rows == 0) continue;
-                t.e = u.e, t.r0 = u.r0, t.rows = u.rows;
-            } else {
+        if constexpr (GROUPED) {
+            if (untaken == 0)
+                run([&](int first, int n, int step) {
+                    const int lane = mx_here(threadIdx.x & 63);
+                    while (untaken == 0 && nth < n) {
+                        int tm, tn;
+                        place(first + min(nth + lane * step, n - 1), tm, tn);
+                        const MxTileEntry u = p.tiles[tn];
+                        mine = MxTile{u.r0, tm * OUTS, u.e, u.rows};
+                        untaken = __ballot(nth + lane * step < n && u.rows > 0);
+                        nth += 64 * step;
+                    }
+                });
+            if (untaken != 0) {
+                const int from = __builtin_ctzll(untaken);
+                untaken &= untaken - 1;
+                t.r0 = __builtin_amdgcn_readlane(mine.r0, from);
+                t.m0 = __builtin_amdgcn_readlane(mine.m0, from);
+                t.e = __builtin_amdgcn_readlane(mine.e, from);
+                t.rows = __builtin_amdgcn_readlane(mine.rows, from);
+            }
+        } else {
+            run([&](int first, int n, int step) {
+                if (nth >= n) return;
+                int tm, tn;
+                place(first + nth, tm, tn);
+                nth += step;
+                t.m0 = tm * OUTS;
                 t.r0 = tn * BN;
                 t.rows = static_cast<int>(min(int64_t(BN), p.N - t.r0));
-            }
-            break;
+            });
         }
         return t;
     };
@@ -348,26 +382,27 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
     const auto x_piece = [&](int lane, int i) { return (lane % XC) ^ mx_swizzle<XC>(x_lds_row(lane, i)); };
     // the tile that is being loaded, and its next stage
     int at = 0;
-    uint32_t *row_table = reinterpret_cast<uint32_t *>(lds + L::table) + wave * (BN / NW);
     const uint8_t *wbase[WI], *xbase;
     int wlen, xlen;
     // this wave's load of scales: rows behind `sbase` of those laid out
     const uint8_t *sbase;
     int64_t srows;           // rows of a stage
     int slen;
-    // grouped: of a tile's rows that this wave loads, one a lane, the pair (asked for
-    // a stage before the tile is opened)
-    const auto table_row = [&](int lane) { return XR * (lane / XR * NW + wave) + lane % XR; };
-    int64_t pair = -1;
-    const auto ask = [&](const MxTile &t) {
-        if constexpr (GROUPED) {
-            const int lane = mx_here(threadIdx.x & 63), row = table_row(lane);
-            if (p.order && lane < BN / NW && row < t.rows) pair = p.order[int64_t(t.r0) + row];
-        }
+    // Gathered rows: of a tile's rows that this wave loads, one a lane, where they begin,
+    // in one of three tables in LDS. A table is asked for two fills before the first
+    // that takes it, as many as have come when a slot is filled anew.
+    int turn = 2;            // the table of the tile that is being loaded
+    const auto later = [&](int tiles) { return turn + tiles < 3 ? turn + tiles : turn + tiles - 3; };
+    static_assert(BN / NW <= 64 && D <= 3, "a lane a row; tables come in time");
+    const auto ask = [&](const MxTile &t, int table, bool wanted) __attribute__((always_inline)) {
+        const int lane = mx_here(threadIdx.x & 63);
+        // (what lies out of range comes as zeros)
+        mx_to_lds4(mx_buffer(p.x_at + t.r0, wanted && gather ? t.rows * 4 : 0), lds + L::table + (wanted ? table * L::tables + wave * 256 : 3 * L::tables),
+                   mx_in_or_out(4 * (XR * (lane / XR * NW + wave) + lane % XR), lane, BN / NW));
     };
     const auto open = [&](const MxTile &t) {
-        const int lane = mx_here(threadIdx.x & 63);
         at = 0;
+        turn = later(1);
         const int outs = min(OUTS, static_cast<int>(p.M) - t.m0);
 #pragma unroll
         for (int i = 0; i < WI; ++i) wbase[i] = p.wc + ((int64_t(t.e) * WI + i) * p.M + t.m0) * wrb;
@@ -380,20 +415,14 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
         sbase = (sofw ? p.ws : p.xs) + srow * kTileScale;
         srows = sofw ? p.ws_rows : p.N;
         slen = static_cast<int>(max(min(srows - srow, sofw ? (WI - 1) * p.M + OUTS : int64_t(BN)), int64_t(0)) * kTileScale);
-        if constexpr (GROUPED) {
-            // where the rows that this wave's loads take begin, one a lane, kept in LDS for all of the tile's stages
-            static_assert(BN / NW <= 64, "a lane a row");
-            const int row = table_row(lane);
-            int64_t x = row;
-            if (p.order) {
-                x = static_cast<uint32_t>(pair) / p.top;
-                if (pair < 0 || pair >= p.N || x >= p.x_rows) x = -1;
-            }
-            if (lane < BN / NW) row_table[lane] = x < 0 || row >= t.rows ? kMxOut : static_cast<uint32_t>(x * xrb);
-            wave_order();
-        }
     };
-    const auto fill = [&](uint8_t *dst, bool real) {
+    MxTile after[2];         // to be opened next, and (grouped) behind that
+    // a lane's scales are of two rows of the weights' LDS rows, or of x's
+    const int silu_soff = SILU ? mx_here(static_cast<int>((sofw ? weight_row(2 * lane) + (lane & 16 ? p.M : 0) : 2 * lane) * kTileScale)) : 0;
+    const uint32_t gathers = GROUPED ? mx_here(gather ? -1 : 0) : 0;
+    // (without branches: a stage is one block of instructions, of which the matrix
+    // instructions are spread over all the others)
+    const auto fill = [&](uint8_t *dst, bool real) __attribute__((always_inline)) {
         const int wk = at * L::wrow, xk0 = at * L::xrow;
         const int wrb = mx_here_scalar(p.K / 2), xrb = static_cast<int>(mx_bytes<XF>(mx_here_scalar(p.K)));
         const int left = p.K - at * kTileK, lane = mx_here(threadIdx.x & 63);
@@ -413,13 +442,20 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
 #pragma unroll
         for (int i = 0; i < XL; ++i) {
             const int q = i * NW + wave, piece = x_piece(lane, i);
-            const uint32_t row = GROUPED ? row_table[XR * i + lane / XC] : static_cast<uint32_t>(lane / XC * xrb + XR * q * xrb);
-            mx_to_lds16(xbuf, dst + L::x + q * 1024, piece * (XF == kMxE2M1 ? 32 : 16) < left ? row + 16 * piece : kMxOut);
+            uint32_t row = static_cast<uint32_t>(lane / XC * xrb + XR * q * xrb);
+            if constexpr (GROUPED) {
+                const uint32_t *table = reinterpret_cast<const uint32_t *>(lds + L::table + turn * L::tables + wave * 256);
+                const uint32_t from = table[XR * i + lane / XC];
+                row = (from & gathers) | (row & ~gathers);
+            }
+            mx_to_lds16(xbuf, dst + L::x + q * 1024, mx_in_or_out(row + 16 * piece, piece * (XF == kMxE2M1 ? 32 : 16), left));
         }
-        // two rows of the weights' LDS rows, or of x's
-        const int srow = 2 * lane;
-        const uint32_t soff = static_cast<uint32_t>((sofw ? weight_row(srow) + (SILU && (srow & 32) ? p.M : 0) : srow) * kTileScale);
-        mx_to_lds16(mx_buffer(sbase + at * srows * kTileScale, real ? slen : 0), dst + L::sw + sload * 1024, soff);
+        mx_to_lds16(mx_buffer(sbase + at * srows * kTileScale, real ? slen : 0), dst + L::sw + sload * 1024,
+                    SILU ? silu_soff : 2 * kTileScale * lane);
+        if constexpr (GROUPED) {
+            const bool each = stages == 1;           // (then the next tile's is here or under way)
+            ask(each ? after[1] : after[0], later(1 + each), each || at + 2 == stages);
+        }
     };
 
     f32x16 acc[TI][TJ];
@@ -436,29 +472,35 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
         ops[0].read(src + wm * L::wrow, src + L::x + wn * L::xrow, 0, r, g);
     };
 
-    // tiles that are loaded, at least in part, behind the current one, and the one after
-    MxTile cur = next_tile(), ahead[D], after{0, 0, 0, 0};
+    // tiles that are loaded, at least in part, behind the current one
+    MxTile cur = next_tile(), ahead[D];
     if (cur.rows == 0) return;
     int waiting = 0;
     bool more = true;
-    ask(cur);
+    after[0] = next_tile();
+    if constexpr (GROUPED) {
+        after[1] = next_tile();
+        ask(cur, 0, true);
+        ask(after[0], 1, true);
+        ask(after[1], 2, true);
+        mx_meet<0>();
+    }
     open(cur);
-    // takes the next stage's tile; looks for the tile after at its last stage
-    const auto advance = [&]() {
+    // takes the next stage's tile
+    const auto advance = [&]() __attribute__((always_inline)) {
+        if (!more || at < stages) return;
+        more = after[0].rows != 0;
         if (!more) return;
-        if (at == stages) {
-            more = after.rows != 0;
-            if (more) {
-                open(after);
+        open(after[0]);
 #pragma unroll
-                for (int i = 0; i < D; ++i)
-                    if (i == waiting) ahead[i] = after;
-                ++waiting;
-            }
-        }
-        if (at == stages - 1) {
-            after = next_tile();
-            ask(after);
+        for (int i = 0; i < D; ++i)
+            if (i == waiting) ahead[i] = after[0];
+        ++waiting;
+        if constexpr (GROUPED) {
+            after[0] = after[1];
+            after[1] = next_tile();
+        } else {
+            after[0] = next_tile();
         }
     };
     for (int d = 0; d < D; ++d) {
@@ -472,7 +514,8 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
     // A step's operands are read while the one before is multiplied. Once the
     // last step's are read the waves meet: then the next stage's first operands
     // are read and the stage's slot is filled anew, beside the last step's products.
-    constexpr int MFMAS = TI * TJ * kXParts<XF>, READS = TI + TJ * kXParts<XF>;
+    constexpr int MFMAS = TI * TJ * kXParts<XF>, READS = TI + TJ * kXParts<XF>, LOADS = WL + XL + 1 + GROUPED;
+    constexpr int STORES = TI / WI * TJ * (sizeof(T) == 4 ? 4 : 2);      // at least, of a tile
     int slot = 0;
     for (;;) {
 #pragma unroll
@@ -481,8 +524,10 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
             for (int j = 0; j < TJ; ++j)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-        for (int t = 0; t < stages; ++t) {
+        // (in the first the last tile's stores come after the last loads)
+        const auto stage = [&](auto first) __attribute__((always_inline)) {
             const uint8_t *wl = lds + slot * L::stage + wm * L::wrow, *xl = lds + slot * L::stage + L::x + wn * L::xrow;
+            advance();
             __builtin_amdgcn_sched_barrier(0);
             ops[1].read(wl, xl, 1, r, g);
             mx_tile_step<0>(ops[0], sw[0], sx[0], acc);
@@ -493,25 +538,22 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
             ops[1].read(wl, xl, 3, r, g);
             mx_tile_step<2>(ops[0], sw[0], sx[0], acc);
             mx_interleave<MFMAS, READS, 0>();
-            // (the first time all of the wave's stores of the last tile are waited for too)
-            if (D == 2 || t == 0)
-                mx_meet<0>();
-            else
-                mx_meet<(D - 2) * (WL + XL + 1)>();
+            mx_meet<(D - 2) * LOADS + (D > 2 && decltype(first)::value ? STORES : 0)>();
+            __builtin_amdgcn_sched_barrier(0);
             const int freed = slot;
             slot = slot + 1 == D ? 0 : slot + 1;
-            advance();
-            __builtin_amdgcn_sched_barrier(0);
             begin(slot, sw[1], sx[1]);
             fill(lds + freed * L::stage, more);
             mx_tile_step<3>(ops[1], sw[0], sx[0], acc);
-            mx_interleave<MFMAS, READS + TI + TJ, WL + XL + 1>();
+            mx_interleave<MFMAS, READS + TI + TJ, LOADS>();
             at += more;
 #pragma unroll
             for (int i = 0; i < TI; ++i) sw[0][i] = sw[1][i];
 #pragma unroll
             for (int j = 0; j < TJ; ++j) sx[0][j] = sx[1][j];
-        }
+        };
+        stage(std::true_type{});
+        for (int t = 1; t < stages; ++t) stage(std::false_type{});
 
         const int outs = min(OUTS, static_cast<int>(p.M) - cur.m0);
         if (p.M % (16 / static_cast<int>(sizeof(T))) == 0)
