@@ -11,8 +11,8 @@ int64_t weight_rows(const MxCall &c) { return c.wide() * (c.grouped ? c.experts 
 int64_t scale_stages(const MxCall &c) { return ceil_div(c.K, kTileK); }
 size_t weight_scale_bytes(const MxCall &c) { return align256(static_cast<size_t>(scale_stages(c)) * weight_rows(c) * kTileScale); }
 size_t row_scale_bytes(const MxCall &c) { return align256(static_cast<size_t>(scale_stages(c)) * c.N * kTileScale); }
-// grouped: the list of tiles, and behind it where the sorted rows' codes begin
-int64_t tile_list(const MxCall &c, int64_t bn) { return static_cast<int64_t>(align256(c.row_tiles(bn) * sizeof(MxTileEntry)) / sizeof(MxTileEntry)); }
+// grouped: the list of tiles and their number, and behind it where the sorted rows' codes begin
+int64_t tile_list(const MxCall &c, int64_t bn) { return static_cast<int64_t>(align256((c.row_tiles(bn) + 1) * sizeof(MxTileEntry)) / sizeof(MxTileEntry)); }
 int64_t scale_workgroups(const MxCall &c, int64_t bn)
 {
     return ceil_div(weight_rows(c), 64) + ceil_div(c.N, 64) + (c.grouped ? ceil_div(c.row_tiles(bn), kScaleThreads) : 0);
@@ -50,17 +50,17 @@ void launch_scales(const MxCall &c, int bn, MxGemmParams &p, void *ws, hipStream
     p.ws_rows = s.wrows;
 }
 
-template <typename F, int BM, int BN, int WM, int WN, int D>
+template <typename F, int BM, int BN, int WM, int WN>
 void launch(const MxCall &c, MxGemmParams p, void *ws, hipStream_t stream)
 {
     launch_scales(c, BN, p, ws, stream);
     p.tiles_m = static_cast<int>(ceil_div(c.M, BM / (F::SILU ? 2 : 1)));
     p.tiles_n = static_cast<int>(c.row_tiles(BN));
     static std::atomic<uint64_t> asked{0};
-    constexpr size_t bytes = MxTileLds<F::XF, F::GROUPED, BM, BN, WM * WN, D>::bytes;
+    constexpr size_t bytes = MxTileLds<F::XF, F::GROUPED, BM, BN, WM * WN>::bytes;
     constexpr int64_t per = 160 * 1024 / bytes;      // workgroups that a compute unit holds
     static_assert(per >= 1, "LDS of a compute unit");
-    const auto kernel = &mx_tile_kernel<F::XF, typename F::T, F::SILU, F::GROUPED, BM, BN, WM, WN, D>;
+    const auto kernel = &mx_tile_kernel<F::XF, typename F::T, F::SILU, F::GROUPED, BM, BN, WM, WN>;
     allow_dynamic_lds(reinterpret_cast<const void *>(kernel), bytes, asked);
     const int64_t grid = std::min(int64_t(p.tiles_m) * p.tiles_n, per * kComputeUnits);
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(64 * WM * WN), bytes, stream, p);
@@ -70,7 +70,7 @@ void launch(const MxCall &c, MxGemmParams p, void *ws, hipStream_t stream)
 
 int64_t mx_tile_rows(const MxCall &c, int size)
 {
-    return size == 256 ? (c.xfmt == QMX_E2M1 && c.act == QMX_NONE && !c.grouped ? 256 : 128) : size;
+    return size == 256 && c.xfmt != QMX_E2M1 ? 128 : size;
 }
 
 size_t mx_tile_workspace(const MxCall &c, int size)
@@ -89,14 +89,10 @@ void mx_launch_tile(const MxCall &c, const MxGemmParams &p, int size, void *ws, 
 {
     mx_dispatch(c, [&](auto form) {
         using F = decltype(form);
-        if (size == 64) return launch<F, 64, 64, 1, 2, 2>(c, p, ws, stream);
-        if (size == 128) return launch<F, 128, 128, 2, 2, 2>(c, p, ws, stream);
-        if constexpr (F::XF == kMxE4M3)
-            return launch<F, 256, 128, 2, 4, 2>(c, p, ws, stream);
-        else if constexpr (F::SILU || F::GROUPED)
-            return launch<F, 256, 128, 4, 2, 3>(c, p, ws, stream);
-        else
-            return launch<F, 256, 256, 2, 4, 2>(c, p, ws, stream);
+        if (size == 64) return launch<F, 64, 64, 1, 2>(c, p, ws, stream);
+        if (size == 128) return launch<F, 128, 128, 2, 2>(c, p, ws, stream);
+        // (of e4m3 rows two slots for 256 x 256 would not fit in LDS)
+        launch<F, 256, F::XF == kMxE4M3 ? 128 : 256, 2, 4>(c, p, ws, stream);
     });
 }
 

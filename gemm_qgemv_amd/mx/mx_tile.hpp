@@ -2,7 +2,7 @@
 // brought from memory straight into LDS.
 //
 // A workgroup of WM x WN waves takes tiles of BM weight rows and BN rows of x in
-// turn; a stage is 256 inputs of both in one of D LDS slots, filled by loads
+// turn; a stage is 256 inputs of both in one of two LDS slots, filled by loads
 // that go to LDS directly while others are multiplied. A wave takes BM / WM x BN
 // / WN of the tile in blocks of 32 x 32. Stages run on from tile to tile: while
 // a tile's results are written the next one's first stages are on their way.
@@ -19,8 +19,6 @@
 // in turn, so that a lane holds both numbers of an output.
 #pragma once
 
-#include <type_traits>
-
 #include "mx_gemm.hpp"
 
 namespace qg {
@@ -28,13 +26,15 @@ namespace qg {
 constexpr int kTileK = 256;      // inputs of a stage
 constexpr int kTileScale = kTileK / kMxBlock;      // bytes of scales of a row and stage
 
-template <int XF, bool GROUPED, int BM, int BN, int NW, int D>
+constexpr int kTileSlots = 2;
+
+template <int XF, bool GROUPED, int BM, int BN, int NW>
 struct MxTileLds {
     static constexpr int wrow = kTileK / 2, xrow = static_cast<int>(mx_bytes<XF>(kTileK));
     static constexpr int wb = (BM + 127) / 128, xb = (BN + 127) / 128;    // loads of scales: 128 rows, 1 KiB
     static constexpr int x = BM * wrow, sw = x + BN * xrow, sx = sw + wb * 1024, stage = sx + xb * 1024;
-    static constexpr int table = D * stage, tables = GROUPED ? NW * 256 : 0;      // where rows of x begin, of three tiles
-    static constexpr int bytes = table + 3 * tables + (GROUPED ? 256 : 0);        // (the last for what nobody wants)
+    static constexpr int table = kTileSlots * stage, tables = GROUPED ? NW * 256 : 0;      // where rows of x begin, of two tiles
+    static constexpr int bytes = table + 2 * tables + (GROUPED ? 256 : 0);        // (the last for what nobody wants)
 };
 
 // 16-byte chunk c of LDS row r lies at chunk c ^ swizzle(r): 16 lanes that
@@ -265,6 +265,8 @@ __device__ __forceinline__ void mx_list_tiles(const MxScalesParams &p, int first
     }
     __syncthreads();
     const int tile = first + threadIdx.x;
+    // behind the list the number of tiles that there are
+    if (tile == 0) p.tiles[p.tiles_n] = MxTileEntry{max(0, min(upto[kMaxExperts - 1], p.tiles_n)), 0, 0, 0};
     if (tile >= p.tiles_n) return;
     int lo = 0, hi = kMaxExperts;                    // the first expert with more tiles up to it
     while (lo < hi) {
@@ -296,11 +298,11 @@ static __global__ __launch_bounds__(kScaleThreads) void mx_scales_kernel(MxScale
         mx_list_tiles(p, (block - p.wblocks - p.xblocks) * kScaleThreads);
 }
 
-template <int XF, typename T, bool SILU, bool GROUPED, int BM, int BN, int WM, int WN, int D>
+template <int XF, typename T, bool SILU, bool GROUPED, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
 {
-    constexpr int NW = WM * WN, TI = BM / WM / 32, TJ = BN / WN / 32, WI = SILU ? 2 : 1;
-    using L = MxTileLds<XF, GROUPED, BM, BN, NW, D>;
+    constexpr int NW = WM * WN, TI = BM / WM / 32, TJ = BN / WN / 32, WI = SILU ? 2 : 1, D = kTileSlots;
+    using L = MxTileLds<XF, GROUPED, BM, BN, NW>;
     static_assert(TI % WI == 0, "a wave holds gate and up rows of an output");
     constexpr int OUTS = BM / WI;                    // outputs of a tile
     extern __shared__ __align__(16) uint8_t lds[];
@@ -316,14 +318,15 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
     // operands for 33 in a row.
     int nth = blockIdx.x >> 3;
     // f(first id of the XCD's run, its end, workgroups of the XCD)
+    const int tiles_n = GROUPED ? p.tiles[p.tiles_n].e : p.tiles_n;
     const auto run = [&](auto f) {
-        const int ntiles = p.tiles_m * p.tiles_n, xcd = blockIdx.x & 7, xcds = min(8, static_cast<int>(gridDim.x));
+        const int ntiles = p.tiles_m * tiles_n, xcd = blockIdx.x & 7, xcds = min(8, static_cast<int>(gridDim.x));
         f(xcd * (ntiles / xcds) + min(xcd, ntiles % xcds), ntiles / xcds + (xcd < ntiles % xcds), (static_cast<int>(gridDim.x) - xcd + 7) >> 3);
     };
     constexpr int BAND = 4;
     const auto place = [&](int id, int &tm, int &tn) {
         const int band = id / (BAND * p.tiles_m), in = id - band * (BAND * p.tiles_m);
-        const int high = min(BAND, p.tiles_n - band * BAND);
+        const int high = min(BAND, tiles_n - band * BAND);
         tm = in / high, tn = band * BAND + in % high;
     };
     // grouped: the workgroup's next 64 tiles, one a lane, and those not taken yet, so that
@@ -389,20 +392,18 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
     int64_t srows;           // rows of a stage
     int slen;
     // Gathered rows: of a tile's rows that this wave loads, one a lane, where they begin,
-    // in one of three tables in LDS. A table is asked for two fills before the first
-    // that takes it, as many as have come when a slot is filled anew.
-    int turn = 2;            // the table of the tile that is being loaded
-    const auto later = [&](int tiles) { return turn + tiles < 3 ? turn + tiles : turn + tiles - 3; };
-    static_assert(BN / NW <= 64 && D <= 3, "a lane a row; tables come in time");
+    // in one of two tables in LDS, asked for one fill before the first that takes it.
+    int turn = 1;            // the table of the tile that is being loaded
+    static_assert(BN / NW <= 64, "a lane a row");
     const auto ask = [&](const MxTile &t, int table, bool wanted) __attribute__((always_inline)) {
         const int lane = mx_here(threadIdx.x & 63);
         // (what lies out of range comes as zeros)
-        mx_to_lds4(mx_buffer(p.x_at + t.r0, wanted && gather ? t.rows * 4 : 0), lds + L::table + (wanted ? table * L::tables + wave * 256 : 3 * L::tables),
+        mx_to_lds4(mx_buffer(p.x_at + t.r0, wanted && gather ? t.rows * 4 : 0), lds + L::table + (wanted ? table * L::tables + wave * 256 : 2 * L::tables),
                    mx_in_or_out(4 * (XR * (lane / XR * NW + wave) + lane % XR), lane, BN / NW));
     };
     const auto open = [&](const MxTile &t) {
         at = 0;
-        turn = later(1);
+        turn ^= 1;
         const int outs = min(OUTS, static_cast<int>(p.M) - t.m0);
 #pragma unroll
         for (int i = 0; i < WI; ++i) wbase[i] = p.wc + ((int64_t(t.e) * WI + i) * p.M + t.m0) * wrb;
@@ -416,7 +417,7 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
         srows = sofw ? p.ws_rows : p.N;
         slen = static_cast<int>(max(min(srows - srow, sofw ? (WI - 1) * p.M + OUTS : int64_t(BN)), int64_t(0)) * kTileScale);
     };
-    MxTile after[2];         // to be opened next, and (grouped) behind that
+    MxTile after;            // to be opened next
     // a lane's scales are of two rows of the weights' LDS rows, or of x's
     const int silu_soff = SILU ? mx_here(static_cast<int>((sofw ? weight_row(2 * lane) + (lane & 16 ? p.M : 0) : 2 * lane) * kTileScale)) : 0;
     const uint32_t gathers = GROUPED ? mx_here(gather ? -1 : 0) : 0;
@@ -452,14 +453,13 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
         }
         mx_to_lds16(mx_buffer(sbase + at * srows * kTileScale, real ? slen : 0), dst + L::sw + sload * 1024,
                     SILU ? silu_soff : 2 * kTileScale * lane);
-        if constexpr (GROUPED) {
-            const bool each = stages == 1;           // (then the next tile's is here or under way)
-            ask(each ? after[1] : after[0], later(1 + each), each || at + 2 == stages);
-        }
+        if constexpr (GROUPED) ask(after, turn ^ 1, at + 1 == stages);
     };
 
     f32x16 acc[TI][TJ];
-    const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
+    // (waves of the same rows next to each other, so that where a tile has half of its
+    // rows every SIMD is left one of its waves)
+    const int wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
     int sw[2][TI], sx[2][TJ];
     MxTileOps<XF, TI, TJ> ops[2];
     // step 0 of the stage in a slot and the stage's scales
@@ -477,31 +477,24 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
     if (cur.rows == 0) return;
     int waiting = 0;
     bool more = true;
-    after[0] = next_tile();
+    after = next_tile();
     if constexpr (GROUPED) {
-        after[1] = next_tile();
         ask(cur, 0, true);
-        ask(after[0], 1, true);
-        ask(after[1], 2, true);
+        ask(after, 1, true);
         mx_meet<0>();
     }
     open(cur);
     // takes the next stage's tile
     const auto advance = [&]() __attribute__((always_inline)) {
         if (!more || at < stages) return;
-        more = after[0].rows != 0;
+        more = after.rows != 0;
         if (!more) return;
-        open(after[0]);
+        open(after);
 #pragma unroll
         for (int i = 0; i < D; ++i)
-            if (i == waiting) ahead[i] = after[0];
+            if (i == waiting) ahead[i] = after;
         ++waiting;
-        if constexpr (GROUPED) {
-            after[0] = after[1];
-            after[1] = next_tile();
-        } else {
-            after[0] = next_tile();
-        }
+        after = next_tile();
     };
     for (int d = 0; d < D; ++d) {
         advance();
@@ -515,51 +508,61 @@ __global__ __launch_bounds__(64 * WM *WN) void mx_tile_kernel(MxGemmParams p)
     // last step's are read the waves meet: then the next stage's first operands
     // are read and the stage's slot is filled anew, beside the last step's products.
     constexpr int MFMAS = TI * TJ * kXParts<XF>, READS = TI + TJ * kXParts<XF>, LOADS = WL + XL + 1 + GROUPED;
-    constexpr int STORES = TI / WI * TJ * (sizeof(T) == 4 ? 4 : 2);      // at least, of a tile
     int slot = 0;
+    const auto stage = [&]() __attribute__((always_inline)) {
+        const uint8_t *wl = lds + slot * L::stage + wm * L::wrow, *xl = lds + slot * L::stage + L::x + wn * L::xrow;
+        advance();
+        __builtin_amdgcn_sched_barrier(0);
+        ops[1].read(wl, xl, 1, r, g);
+        mx_tile_step<0>(ops[0], sw[0], sx[0], acc);
+        mx_interleave<MFMAS, READS, 0>();
+        ops[0].read(wl, xl, 2, r, g);
+        mx_tile_step<1>(ops[1], sw[0], sx[0], acc);
+        mx_interleave<MFMAS, READS, 0>();
+        ops[1].read(wl, xl, 3, r, g);
+        mx_tile_step<2>(ops[0], sw[0], sx[0], acc);
+        mx_interleave<MFMAS, READS, 0>();
+        mx_meet<0>();
+        __builtin_amdgcn_sched_barrier(0);
+        const int freed = slot;
+        slot = slot + 1 == D ? 0 : slot + 1;
+        begin(slot, sw[1], sx[1]);
+        fill(lds + freed * L::stage, more);
+        mx_tile_step<3>(ops[1], sw[0], sx[0], acc);
+        mx_interleave<MFMAS, READS + TI + TJ, LOADS>();
+        at += more;
+#pragma unroll
+        for (int i = 0; i < TI; ++i) sw[0][i] = sw[1][i];
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) sx[0][j] = sx[1][j];
+    };
+    // a wave that has no rows of the tile brings its share of the loads
+    const auto idle_stage = [&]() __attribute__((always_inline)) {
+        advance();
+        mx_meet<0>();
+        const int freed = slot;
+        slot = slot + 1 == D ? 0 : slot + 1;
+        begin(slot, sw[0], sx[0]);
+        fill(lds + freed * L::stage, more);
+        at += more;
+    };
     for (;;) {
+        if (wn < cur.rows) {
 #pragma unroll
-        for (int i = 0; i < TI; ++i)
+            for (int i = 0; i < TI; ++i)
 #pragma unroll
-            for (int j = 0; j < TJ; ++j)
+                for (int j = 0; j < TJ; ++j)
 #pragma unroll
-                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-        // (in the first the last tile's stores come after the last loads)
-        const auto stage = [&](auto first) __attribute__((always_inline)) {
-            const uint8_t *wl = lds + slot * L::stage + wm * L::wrow, *xl = lds + slot * L::stage + L::x + wn * L::xrow;
-            advance();
-            __builtin_amdgcn_sched_barrier(0);
-            ops[1].read(wl, xl, 1, r, g);
-            mx_tile_step<0>(ops[0], sw[0], sx[0], acc);
-            mx_interleave<MFMAS, READS, 0>();
-            ops[0].read(wl, xl, 2, r, g);
-            mx_tile_step<1>(ops[1], sw[0], sx[0], acc);
-            mx_interleave<MFMAS, READS, 0>();
-            ops[1].read(wl, xl, 3, r, g);
-            mx_tile_step<2>(ops[0], sw[0], sx[0], acc);
-            mx_interleave<MFMAS, READS, 0>();
-            mx_meet<(D - 2) * LOADS + (D > 2 && decltype(first)::value ? STORES : 0)>();
-            __builtin_amdgcn_sched_barrier(0);
-            const int freed = slot;
-            slot = slot + 1 == D ? 0 : slot + 1;
-            begin(slot, sw[1], sx[1]);
-            fill(lds + freed * L::stage, more);
-            mx_tile_step<3>(ops[1], sw[0], sx[0], acc);
-            mx_interleave<MFMAS, READS + TI + TJ, LOADS>();
-            at += more;
-#pragma unroll
-            for (int i = 0; i < TI; ++i) sw[0][i] = sw[1][i];
-#pragma unroll
-            for (int j = 0; j < TJ; ++j) sx[0][j] = sx[1][j];
-        };
-        stage(std::true_type{});
-        for (int t = 1; t < stages; ++t) stage(std::false_type{});
-
-        const int outs = min(OUTS, static_cast<int>(p.M) - cur.m0);
-        if (p.M % (16 / static_cast<int>(sizeof(T))) == 0)
-            mx_tile_store<T, SILU, true>(acc, static_cast<T *>(p.y) + int64_t(cur.r0) * p.M + cur.m0, p.M, cur.rows, outs, wn, wm / WI);
-        else
-            mx_tile_store<T, SILU, false>(acc, static_cast<T *>(p.y) + int64_t(cur.r0) * p.M + cur.m0, p.M, cur.rows, outs, wn, wm / WI);
+                    for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+            for (int t = 0; t < stages; ++t) stage();
+            const int outs = min(OUTS, static_cast<int>(p.M) - cur.m0);
+            if (p.M % (16 / static_cast<int>(sizeof(T))) == 0)
+                mx_tile_store<T, SILU, true>(acc, static_cast<T *>(p.y) + int64_t(cur.r0) * p.M + cur.m0, p.M, cur.rows, outs, wn, wm / WI);
+            else
+                mx_tile_store<T, SILU, false>(acc, static_cast<T *>(p.y) + int64_t(cur.r0) * p.M + cur.m0, p.M, cur.rows, outs, wn, wm / WI);
+        } else {
+            for (int t = 0; t < stages; ++t) idle_stage();
+        }
         if (waiting == 0) break;
         cur = ahead[0];
 #pragma unroll
