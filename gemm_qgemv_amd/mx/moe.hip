@@ -5,28 +5,31 @@
 #include <algorithm>
 
 #include "combine.hpp"
-#include "plan_experts.hpp"
 #include "route.hpp"
 
 namespace {
+
+// Logits of a lane up to which router and sort are one launch (the waves of a workgroup of
+// 1024 threads have 128 registers).
+constexpr int kFusedLogits = 16;
 
 struct Sort {
     int64_t run;
     int runs;
 };
 
-// Runs of 4096 pairs, and no more of them than kSortMaxRuns.
+// Runs of 2048 pairs, and no more of them than kSortMaxRuns.
 Sort plan_sort(int64_t pairs)
 {
     const int64_t unit = 64 * qg::kSortWaves;
-    const int64_t run = std::max<int64_t>(4 * unit, round_up(ceil_div(pairs, qg::kSortMaxRuns), unit));
+    const int64_t run = std::max<int64_t>(qg::kSortSteps * unit, round_up(ceil_div(pairs, qg::kSortMaxRuns), unit));
     return Sort{run, static_cast<int>(std::max<int64_t>(1, ceil_div(pairs, run)))};
 }
 
 size_t sort_bytes(const Sort &s, int experts) { return s.runs == 1 ? 0 : align256(static_cast<size_t>(s.runs) * experts * 4); }
 
-void launch_sort(const Sort &s, const int32_t *ids, int64_t pairs, int experts, int32_t *offsets, int32_t *order, int32_t *slots, void *ws,
-                 hipStream_t stream)
+qg::SortParams sort_params(const Sort &s, const int32_t *ids, int64_t pairs, int experts, int32_t *offsets, int32_t *order, int32_t *slots,
+                           void *ws)
 {
     qg::SortParams p{};
     p.ids = ids;
@@ -39,12 +42,19 @@ void launch_sort(const Sort &s, const int32_t *ids, int64_t pairs, int experts, 
     p.offsets = offsets;
     p.order = order;
     p.slots = slots;
-    const size_t width = (static_cast<size_t>(experts) + 1) * 4;
-    if (s.runs > 1)
-        hipLaunchKernelGGL(qg::sort_count_kernel, dim3(static_cast<unsigned>(s.runs)), dim3(qg::kSortThreads), width, stream, p);
+    return p;
+}
+
+size_t sort_lds(int experts) { return static_cast<size_t>(qg::sort_place_ints(experts)) * 4; }
+
+void launch_sort(const qg::SortParams &p, hipStream_t stream)
+{
+    if (p.runs > 1)
+        hipLaunchKernelGGL(qg::sort_count_kernel, dim3(static_cast<unsigned>(p.runs)), dim3(qg::kSortThreads), (static_cast<size_t>(p.experts) + 1) * 4,
+                           stream, p);
     static std::atomic<uint64_t> asked{0};
-    allow_dynamic_lds(reinterpret_cast<const void *>(&qg::sort_place_kernel), (size_t(QMOE_MAX_EXPERTS) + 1) * 4 * qg::kSortWaves, asked);
-    hipLaunchKernelGGL(qg::sort_place_kernel, dim3(static_cast<unsigned>(s.runs)), dim3(qg::kSortThreads), width * qg::kSortWaves, stream, p);
+    allow_dynamic_lds(reinterpret_cast<const void *>(&qg::sort_place_kernel), sort_lds(QMOE_MAX_EXPERTS), asked);
+    hipLaunchKernelGGL(qg::sort_place_kernel, dim3(static_cast<unsigned>(p.runs)), dim3(qg::kSortThreads), sort_lds(p.experts), stream, p);
 }
 
 // Checks that the router and the plan share; `need` is the workspace's size.
@@ -64,15 +74,31 @@ int check_plan(const int32_t *ids, int64_t rows, int experts, int top, const int
     return QG_OK;
 }
 
-template <typename T>
-void launch_route(const qg::RouteParams &p, dim3 grid, hipStream_t stream)
+template <typename T, int V>
+void launch_route(const qg::RouteParams &p, const qg::SortParams &s, hipStream_t stream)
 {
-    const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(qg::kRouteThreads), 0, stream, p); };
-    if (p.experts <= 64) go(qg::route_kernel<T, 4>);
-    else if (p.experts <= 128) go(qg::route_kernel<T, 8>);
-    else if (p.experts <= 256) go(qg::route_kernel<T, 16>);
-    else if (p.experts <= 512) go(qg::route_kernel<T, 32>);
-    else go(qg::route_kernel<T, 64>);
+    // One workgroup for both, where the rows are no more than it takes at once.
+    if constexpr (V <= kFusedLogits) {
+        if (p.rows <= qg::kRouteSortRows && s.runs == 1) {
+            static std::atomic<uint64_t> asked{0};
+            allow_dynamic_lds(reinterpret_cast<const void *>(&qg::route_sort_kernel<T, V>), sort_lds(16 * V), asked);
+            hipLaunchKernelGGL((qg::route_sort_kernel<T, V>), dim3(1), dim3(qg::kSortThreads), sort_lds(p.experts), stream, p, s);
+            return;
+        }
+    }
+    if (p.rows > 0)
+        hipLaunchKernelGGL((qg::route_kernel<T, V>), dim3(static_cast<unsigned>(ceil_div(p.rows, qg::kRouteRows))), dim3(qg::kRouteThreads), 0, stream, p);
+    launch_sort(s, stream);
+}
+
+template <typename T>
+void launch_route(const qg::RouteParams &p, const qg::SortParams &s, hipStream_t stream)
+{
+    if (p.experts <= 64) launch_route<T, 4>(p, s, stream);
+    else if (p.experts <= 128) launch_route<T, 8>(p, s, stream);
+    else if (p.experts <= 256) launch_route<T, 16>(p, s, stream);
+    else if (p.experts <= 512) launch_route<T, 32>(p, s, stream);
+    else launch_route<T, 64>(p, s, stream);
 }
 
 }  // namespace
@@ -97,7 +123,7 @@ int qmoe_plan(const int32_t *ids, int64_t rows, int experts, int top, int32_t *o
     st = check_alias(&in, 1, out, 4);
     if (st != QG_OK) return st;
     (void)hipGetLastError();
-    launch_sort(plan_sort(pairs), ids, pairs, experts, offsets, order, slots, ws, stream);
+    launch_sort(sort_params(plan_sort(pairs), ids, pairs, experts, offsets, order, slots, ws), stream);
     return launch_status();
 }
 
@@ -120,12 +146,9 @@ int qmoe_route(int dtype, const void *logits, int64_t ld, int64_t rows, int expe
     if (st != QG_OK) return st;
 
     (void)hipGetLastError();
-    if (rows > 0) {
-        const qg::RouteParams p{logits, ld, rows, experts, top, renorm != 0, ids, weights};
-        const dim3 grid(static_cast<unsigned>(ceil_div(rows, qg::kRouteRows)));
-        dtype == QG_F32 ? launch_route<float>(p, grid, stream) : launch_route<uint16_t>(p, grid, stream);
-    }
-    launch_sort(plan_sort(pairs), ids, pairs, experts, offsets, order, slots, ws, stream);
+    const qg::RouteParams p{logits, ld, rows, experts, top, renorm != 0, ids, weights};
+    const qg::SortParams sort = sort_params(plan_sort(pairs), ids, pairs, experts, offsets, order, slots, ws);
+    dtype == QG_F32 ? launch_route<float>(p, sort, stream) : launch_route<uint16_t>(p, sort, stream);
     return launch_status();
 }
 

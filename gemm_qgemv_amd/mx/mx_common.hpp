@@ -70,6 +70,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_buffer(const void *base, in
 }
 constexpr uint32_t kMxOut = 0x80000000u;   // above every range used here
 
+constexpr int kMaxExperts = 1024;
+
 // A wave's 64 pieces of 16 (or 4) bytes, each from its lane's offset, to LDS
 // behind `dst`, one behind the other. (Plain functions: in a template the builtins
 // keep the compiler's host pass from emitting the kernel.)

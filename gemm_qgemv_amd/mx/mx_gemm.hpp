@@ -98,8 +98,6 @@ struct GroupTile {
     int e, r0, r1;
 };
 
-constexpr int kMaxExperts = 1024;
-
 template <int T>
 __device__ __forceinline__ GroupTile group_tile(const int32_t *offsets, int experts, int64_t pairs, int item)
 {

@@ -7,7 +7,7 @@
 // lowest index that has it by four minima.
 #pragma once
 
-#include "mx_common.hpp"
+#include "plan_experts.hpp"
 
 namespace qg {
 
@@ -46,26 +46,27 @@ __device__ __forceinline__ float from_order_bits(uint32_t u)
     return __uint_as_float((u & 0x80000000u) ? u & 0x7fffffffu : ~u);
 }
 
-// V: logits a lane (16 V >= experts).
+// 16 lanes' row. V: logits a lane (16 V >= experts).
 template <typename T, int V>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteParams p)
+__device__ __forceinline__ void route_row(const RouteParams &p, int64_t row)
 {
-    const int64_t row = int64_t(blockIdx.x) * kRouteRows + (threadIdx.x >> 4);
-    if (row >= p.rows) return;                        // 16 lanes leave together
     const int sub = threadIdx.x & 15;
     const T *x = static_cast<const T *>(p.x) + row * p.ld;
+    T t[V];
+    // (under no condition, so that all are on their way together)
+#pragma unroll
+    for (int v = 0; v < V; ++v) t[v] = x[min(v * 16 + sub, p.experts - 1)];
     uint32_t key[V];
     bool bad = false;                                 // a NaN or +infinity
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int e = v * 16 + sub;
-        uint32_t bits = 0xff800000u;                  // -infinity
-        if (e < p.experts) {
-            if constexpr (sizeof(T) == 4)
-                bits = __float_as_uint(x[e]);
-            else
-                bits = static_cast<uint32_t>(x[e]) << 16;
-        }
+        uint32_t bits;
+        if constexpr (sizeof(T) == 4)
+            bits = __float_as_uint(t[v]);
+        else
+            bits = static_cast<uint32_t>(t[v]) << 16;
+        if (e >= p.experts) bits = 0xff800000u;       // -infinity
         const bool none = bits == 0xff800000u;
         bad |= !none && (bits & 0x7fffffffu) >= 0x7f800000u;
         key[v] = none ? 0 : float_order_bits(__uint_as_float(bits));
@@ -118,6 +119,26 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteParams p)
             p.weights[row * p.top + j] = bad ? __builtin_nanf("") : w[h] * inv;
         }
     }
+}
+
+template <typename T, int V>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteParams p)
+{
+    const int64_t row = int64_t(blockIdx.x) * kRouteRows + (threadIdx.x >> 4);
+    if (row < p.rows) route_row<T, V>(p, row);        // (16 lanes alike)
+}
+
+// Router and sort of what one workgroup takes, in one launch.
+constexpr int kRouteSortRows = kSortThreads / 16;
+
+template <typename T, int V>
+__global__ __launch_bounds__(kSortThreads) void route_sort_kernel(RouteParams p, SortParams s)
+{
+    extern __shared__ int32_t lds[];
+    const int row = threadIdx.x >> 4;
+    if (row < p.rows) route_row<T, V>(p, row);
+    __syncthreads();                                  // the ids are there for all of the workgroup
+    sort_place(s, lds);
 }
 
 }  // namespace qg
