@@ -62,7 +62,7 @@ void mx_launch_few(const MxCall &c, const MxGemmParams &p, int blocks, int waves
 // and 6, or where mi is 4 mx_mid_most: more would not fit in registers)
 constexpr int mx_mid_most(int xfmt) { return xfmt == QMX_E2M1 ? 6 : 5; }
 void mx_launch_mid(const MxCall &c, const MxGemmParams &p, int mi, int nj, hipStream_t stream);
-// size: 64, 128 or 256, the tile's weight rows
+// size: 64, 128 (of e2m1 rows only) or 256, the tile's weight rows
 void mx_launch_tile(const MxCall &c, const MxGemmParams &p, int size, void *ws, hipStream_t stream);
 
 // Rows of x in a tile of `size` weight rows, and what its launches need.

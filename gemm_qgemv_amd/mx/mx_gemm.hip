@@ -23,6 +23,12 @@ int64_t usual_rows(const Call &c) { return c.grouped ? ceil_div(c.N, c.experts) 
 //  mid against tiles   17408 x 5120 x 60: 34, 45 [21, 27]; x 90: 45, 45 [24, 28]
 //  mid of 64 weight rows a wave pair against 128   6144 x 2048 x 60: 11, 15 [8, 11];
 //                      17408 x 5120 x 77: 45, 37 [27, 22]
+//  tiles of 64, 128 and 256 (of e4m3 256 x 128), and how full the rounds of the last are
+//                      17408 x 5120 x 120: 45, 50, 63 at 27% [25, 26, 34 at 27%]
+//                      6144 x 2048 x 1000: 39, 43, 33 at 75% [22, 19, 25 at 38%]
+//                      6144 x 2048 x 4000: 127, 117, 83 at 100% [54, 42, 45 at 75%]
+//                      17408 x 5120 x 2048: 415, 381, 290 at 85% [164, 121, 135 at 71%]
+//                      5120 x 17408 x 512: 125, 139, 180 at 31% [63, 65, 112 at 16%]
 Choice choose(const Call &c)
 {
     const int64_t rows = usual_rows(c), wide = c.wide();
@@ -43,9 +49,15 @@ Choice choose(const Call &c)
         const int most = qg::mx_mid_most(c.xfmt);
         if (rows <= 16 * most) return {Choice::kMid, 4, std::min(nj, most)};
     }
-    const auto tiles = [&](int size) { return ceil_div(wide, size) * c.row_tiles(qg::mx_tile_rows(c, size)); };
-    if (tiles(256) >= 2 * kComputeUnits) return {Choice::kTile, 256, 0};
-    if (tiles(128) >= kComputeUnits) return {Choice::kTile, 128, 0};
+    // The largest tiles where their rounds over the compute units are full enough for what
+    // they save to show (in the grouped form half of an expert's last tile is empty).
+    const auto tiles = [&](int size) {
+        const int64_t T = qg::mx_tile_rows(c, size), some = std::min<int64_t>(c.experts, c.N);
+        return ceil_div(wide, size) * (c.grouped ? std::min(c.N, ceil_div(c.N, T) + some / 2) : ceil_div(c.N, T));
+    };
+    const bool e2m1 = c.xfmt == QMX_E2M1;
+    if (tiles(256) * 100 >= round_up(tiles(256), kComputeUnits) * (e2m1 ? 80 : 65)) return {Choice::kTile, 256, 0};
+    if (e2m1 && tiles(128) >= kComputeUnits) return {Choice::kTile, 128, 0};
     return {Choice::kTile, 64, 0};
 }
 

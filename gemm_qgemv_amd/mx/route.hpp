@@ -4,7 +4,10 @@
 // 16 lanes take a row (one DPP row: maxima over it need no LDS), a lane every
 // 16th logit as an order-preserving integer, 0 for what cannot be chosen. Each
 // of the `top` rounds takes the largest number by four DPP maxima, then the
-// lowest index that has it by four minima.
+// lowest index that has it by four minima. Bound by these instructions, not by
+// memory: 16411 x 256 bf16, 6 each, 13.6 us for 9 MB. (Lanes that sort their logits in a
+// network first took three times as long: the conditions held for 16 numbers
+// at once do not fit in the scalar registers.)
 #pragma once
 
 #include "plan_experts.hpp"
@@ -128,7 +131,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteParams p)
     if (row < p.rows) route_row<T, V>(p, row);        // (16 lanes alike)
 }
 
-// Router and sort of what one workgroup takes, in one launch.
+// Router and sort of what one workgroup takes, in one launch (64 x 128, 8 each: 9.2 us
+// of latencies against 4.8 and 5.4 in two).
 constexpr int kRouteSortRows = kSortThreads / 16;
 
 template <typename T, int V>

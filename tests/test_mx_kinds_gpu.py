@@ -36,7 +36,7 @@ def check_wide(got, x, w, xfmt, silu, dtype):
 # and 256; and both sides of where the smallest pieces give way
 KINDS = [(17, 8210), (32, 8196), (17, 16400), (32, 17408), (33, 5480), (64, 4102), (60, 17002), (64, 16386), (65, 3290), (77, 2740), (80, 16394), (77, 17408),
          (81, 16390), (90, 3002), (96, 2736), (96, 17002), (90, 16386),
-         (97, 2400), (150, 1700), (129, 2050), (250, 1030), (700, 6146), (1030, 4100), (2000, 9000), (4100, 8194),
+         (97, 2400), (150, 1700), (129, 2050), (250, 1030), (700, 6146), (1030, 4100), (2000, 9000), (4100, 8194), (1000, 16004), (1900, 8190),
          (64, 4096), (16, 20002), (128, 2048), (256, 1024), (1024, 256), (1030, 262)]
 
 
@@ -124,6 +124,28 @@ def test_experts_of_every_kind(rows, experts, top, wide, kind):
             at = order[a:b] // top if gather else np.arange(a, b)
             check_wide(got[a:b], [t[at] for t in x], [t[e * M * (1 + silu):(e + 1) * M * (1 + silu)] for t in w], xfmt, silu, dtype)
     assert (raw[offsets[-1]:] == 0xA5).all(), "rows behind the last are left as they were"
+
+
+@pytest.mark.parametrize("xfmt", [E2M1, E4M3])
+@pytest.mark.parametrize("silu", [0, 1])
+@pytest.mark.parametrize("rows,experts,top,wide,K", [(4000, 16, 4, 1790, 416), (2040, 8, 2, 3070, 800), (2040, 8, 2, 3070, 256), (4001, 60, 4, 1540, 544)])
+def test_experts_in_the_largest_tiles(rows, experts, top, wide, K, silu, xfmt):
+    rng = rng_for(67, rows, experts, wide, K, silu, xfmt)
+    M = wide // (1 + silu)
+    ids = shares(rng, rows, experts, top, "skewed")
+    offsets, order, _ = ref.plan(ids, experts)
+    for gather in (0, 1):
+        x = operand(rng, rows if gather else rows * top, K, xfmt)
+        w = operand(rng, experts * M * (1 + silu), K, E2M1)
+        if silu:
+            x[1][:] -= 8
+        got, raw = run_experts(x, w, xfmt, offsets, order if gather else None, rows, experts, top, silu, BF16, M, K)
+        for e in range(experts):
+            a, b = offsets[e], offsets[e + 1]
+            if a < b:
+                at = order[a:b] // top if gather else np.arange(a, b)
+                check_wide(got[a:b], [t[at] for t in x], [t[e * M * (1 + silu):(e + 1) * M * (1 + silu)] for t in w], xfmt, silu, BF16)
+        assert (raw[offsets[-1]:] == 0xA5).all()
 
 
 @pytest.mark.parametrize("xfmt", [E2M1, E4M3])
