@@ -157,6 +157,37 @@ def test_workspace_sizes():
     assert q.qmoe_gemm_workspace_bytes(q.QMX_E2M1, 0, 4, 0, 2, 64, 256) == 0
 
 
+LARGE = dict(M=4096, K=256, N=4096)
+FAR = 1 << 40
+
+
+def test_products_in_tiles_need_a_workspace():
+    for xfmt in (q.QMX_E2M1, q.QMX_E4M3):
+        for act in (q.QMX_NONE, q.QMX_SILU_MUL):
+            need = q.qmx_gemm_workspace_bytes(xfmt, act, 4096, 256, 4096)
+            assert need >= (4096 * (1 + act) + 4096) * 8        # both operands' scales
+            call = dict(xfmt=xfmt, act=act, **LARGE)
+            for status, more in ((q.QG_ERR_WORKSPACE, dict(ws=None, ws_bytes=need)), (q.QG_ERR_WORKSPACE, dict(ws=FAR, ws_bytes=need - 1)),
+                                 (q.QG_ERR_ALIGN, dict(ws=FAR + 4, ws_bytes=need))):
+                assert err(q.qmx_gemm, GEMM, **call, **more) == status
+            # apart from each other, and then the workspace over each of them
+            apart = dict(x_codes=FAR, x_scales=FAR + (1 << 28), w_codes=FAR + (2 << 28), w_scales=FAR + (3 << 28), y=FAR + (4 << 28))
+            for name in apart:
+                assert err(q.qmx_gemm, GEMM, **{**call, **apart}, ws=apart[name], ws_bytes=need) == q.QG_ERR_ALIAS
+
+
+def test_experts_in_tiles_need_a_workspace():
+    need = q.qmoe_gemm_workspace_bytes(q.QMX_E2M1, 0, 2048, 8, 2, 4096, 256)
+    assert need >= (8 * 4096 + 4096) * 8 + 4096 * 4             # scales, and where the sorted rows begin
+    call = dict(xfmt=q.QMX_E2M1, act=0, rows=2048, experts=8, top=2, M=4096, K=256)
+    for status, more in ((q.QG_ERR_WORKSPACE, dict(ws=None, ws_bytes=need)), (q.QG_ERR_WORKSPACE, dict(ws=FAR, ws_bytes=need - 1)),
+                         (q.QG_ERR_ALIGN, dict(ws=FAR + 8, ws_bytes=need))):
+        assert err(q.qmoe_gemm, MOE, **call, **more) == status
+    apart = {name: FAR + (i << 28) for i, name in enumerate(("x_codes", "x_scales", "w_codes", "w_scales", "y", "offsets", "order"))}
+    for name in apart:
+        assert err(q.qmoe_gemm, MOE, **call, **apart, ws=apart[name], ws_bytes=need) == q.QG_ERR_ALIAS
+
+
 # ---- the reference forms --------------------------------------------------
 
 def test_reference_quantizer_by_hand():

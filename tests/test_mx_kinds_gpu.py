@@ -212,3 +212,52 @@ def test_operands_at_the_least_alignment():
             q.qmx_gemm(xfmt, moved(x[0], 16), moved(x[1], 4), moved(w[0], 16), moved(w[1], 4), 0, F32, y.t, M, K, N, ws)
             want = wide_values(*map(dev, x), xfmt) @ wide_values(*map(dev, w), E2M1).T.contiguous()
             assert bool((dev(y.check()) == want.float()).all())
+
+
+def random_operand(seed, rows, K, fmt):
+    """operand on the GPU, for more bytes than the host should make."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    codes = torch.empty(rows, ref.row_bytes(fmt, K), dtype=torch.uint8, device="cuda")
+    for part in codes.split(max(1, (1 << 30) // codes.shape[1])):
+        part.copy_(torch.randint(0, 126 if fmt == E4M3 else 256, part.shape, generator=g, device="cuda", dtype=torch.uint8))
+    scales = torch.randint(118, 130, (rows, ref.pitch(K)), generator=g, device="cuda", dtype=torch.uint8)
+    return codes, scales
+
+
+@pytest.mark.parametrize("xfmt,N,M,K,ends", [(E2M1, 3, 131080, 65536, "w"), (E4M3, 40, 131080, 65536, "w"), (E2M1, 130, 131080, 65536, "w"),
+                                             (E4M3, 70001, 72, 65536, "x"), (E2M1, 140001, 8200, 64, "y"), (E4M3, 20, 7000000, 64, "M")])
+def test_product_behind_four_gib(xfmt, N, M, K, ends):
+    """Operands or outputs of more than 4 GiB (and as many outputs a row as there may be,
+    nearly): the first and the last rows and columns."""
+    x, w = random_operand(1, N, K, xfmt), random_operand(2, M, K, E2M1)
+    y = torch.full((N, M), float("nan"), device="cuda")
+    need = q.qmx_gemm_workspace_bytes(xfmt, 0, M, K, N)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda") if need else None
+    q.qmx_gemm(xfmt, *x, *w, 0, F32, y, M, K, N, ws)
+    for rows in (slice(0, 70), slice(max(0, N - 70), N)):
+        for columns in (slice(0, 300), slice(M - 300, M) if M > 300 else slice(0, M)):
+            xv, wv = wide_values(x[0][rows], x[1][rows], xfmt), wide_values(w[0][columns], w[1][columns], E2M1)
+            e = (xv.abs() @ wv.abs().T.contiguous()) * ref.sums_bound(K)
+            assert bool(((y[rows, columns].double() - xv @ wv.T.contiguous()).abs() <= e).all())
+    assert not bool(torch.isnan(y[:, ::997]).any()) and not bool(torch.isnan(y[::997]).any())
+
+
+@pytest.mark.parametrize("rows", [5, 2100, 5000])
+def test_experts_weights_behind_four_gib(rows):
+    experts, top, M, K = 40, 1, 16400, 16384
+    x, w = random_operand(3, rows, K, E2M1), random_operand(4, experts * M, K, E2M1)
+    ids = np.full((rows, top), experts - 1, np.int32)
+    ids[:rows // 2] = 35
+    offsets, order, _ = ref.plan(ids, experts)
+    y = torch.full((rows, M), float("nan"), device="cuda")
+    need = q.qmoe_gemm_workspace_bytes(E2M1, 0, rows, experts, top, M, K)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda") if need else None
+    q.qmoe_gemm(E2M1, *x, *w, dev(offsets), dev(order), rows, experts, top, 0, F32, y, M, K, ws)
+    for e, some in ((35, [0, rows // 2 - 1]), (39, [rows // 2, rows - 1])):
+        xv = wide_values(x[0][some], x[1][some], E2M1)
+        for columns in (slice(0, 300), slice(M - 300, M)):
+            at = slice(e * M + columns.start, e * M + columns.stop)
+            wv = wide_values(w[0][at], w[1][at], E2M1)
+            e_ = (xv.abs() @ wv.abs().T.contiguous()) * ref.sums_bound(K)
+            assert bool(((y[some, columns].double() - xv @ wv.T.contiguous()).abs() <= e_).all())
+    assert not bool(torch.isnan(y).any())
