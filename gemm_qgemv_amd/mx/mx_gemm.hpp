@@ -161,24 +161,29 @@ __device__ __forceinline__ float silu_mul_bf16(float g, float u)
     return g * __builtin_amdgcn_rcpf(1.0f + t) * u;
 }
 
-// g / (1 + exp(-g)) * u. With t = exp(-|g|), which does not overflow, the factor is
-// 1 / (1 + t), or t / (1 + t) where g < 0. t = 2^p (1 + e ln 2), p the float32
-// nearest -|g| log2(e) and e what that leaves out; below 2^-64 it is held times
-// 2^64 (p + 64 is exact there), and the reciprocal of 1..2 is refined once: 8
-// roundings in all.
+// g / (1 + exp(-g)) * u, wherever the result is a float32. With t = exp(-|g|), which
+// does not overflow, the factor is 1 / (1 + t), or t / (1 + t) where g < 0. t = 2^p
+// (1 + e ln 2), p the float32 nearest -|g| log2(e) and e what that leaves out. A t
+// below 2^-64 of a negative g is held as 2^(p - n), n whole, and 2^n comes last:
+// u may be as large as t is small (u less 2^16 in between, so that 200 |u| is in
+// range: exact, or the result is 0). Below g = -200 the result is 0 for every u.
+// The reciprocal of 1..2 is refined once: 8 roundings in all. Not contracted: e
+// belongs to the rounded p.
 __device__ __forceinline__ float silu_mul(float g, float u)
 {
+#pragma clang fp contract(off)
     constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
     const float a = fminf(fabsf(g), 200.0f), p = a * -kLog2e;
     const float e = fmaf(a, -kLog2eLow, fmaf(a, -kLog2e, -p));
-    const bool tiny = p < -64.0f;
-    const float size = tiny ? 0x1p-64f : 1.0f;
-    float t = __builtin_amdgcn_exp2f(tiny ? p + 64.0f : p);
+    const bool tiny = g < 0.0f && p < -64.0f;
+    const float n = tiny ? __builtin_rintf(p) : 0.0f;
+    float t = __builtin_amdgcn_exp2f(p - n);
     t = fmaf(t, e * kLn2, t);
-    const float d = fmaf(t, size, 1.0f);
+    const float d = tiny ? 1.0f : 1.0f + t;
     float q = __builtin_amdgcn_rcpf(d);
     q = fmaf(fmaf(-d, q, 1.0f), q, q);
-    return g < 0.0f ? t * q * g * u * size : q * g * u;
+    const float v = (g < 0.0f ? t * q : q) * g * (u * (!tiny ? 1.0f : g < -200.0f ? 0.0f : 0x1p-16f));
+    return __builtin_ldexpf(v, tiny ? static_cast<int>(n) + 16 : 0);
 }
 
 }  // namespace qg
