@@ -555,7 +555,9 @@ int qmx_dequant(int fmt, const void *codes, const void *scales, int64_t rows, in
  * qmx_gemm -- product of MX rows with MX weights, from one row to long prompts.
  *   y[n][m] = sum over k of x[n][k] * w[m][k],  0 <= n < N, 0 <= m < M,
  * with QMX_SILU_MUL W has 2 M rows, and of g from rows 0..M-1 and u from rows
- * M..2M-1, both float32 sums,  y = g / (1 + exp(-g)) * u.
+ * M..2M-1, both float32 sums,  y = g / (1 + exp(-g)) * u  (of these sums within
+ * 8 roundings to float32 for QG_F32; for QG_BF16 within 2^-15 |y| + 2^-246 |u|
+ * and the rounding to it; NaN where g is -infinity).
  * Products of elements and scales are exact; sums are float32, where an
  * instruction adds the products of 64 or 128 inputs at once and keeps 24
  * bits below the largest of them and the sum: every output is within

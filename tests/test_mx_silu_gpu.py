@@ -74,6 +74,27 @@ def test_silu_float32(N, M, xfmt, kind):
     assert close(run_gemm(x, w, xfmt, M, K, N, 1, F32), want, e).all()
 
 
+@pytest.mark.parametrize("kind", ["large", "any", "small"])
+@pytest.mark.parametrize("xfmt", [E2M1, E4M3])
+@pytest.mark.parametrize("N,M", SIZES)
+def test_silu_bfloat16(N, M, xfmt, kind):
+    rng = rng_for(72, N, M, xfmt, len(kind))
+    x, w, g, u = operands(rng, N, M, xfmt, kind)
+    want = factor(g) * u
+    if kind == "large" and M > 500:
+        assert ((g < -89) & (np.abs(want) > 1e-30)).any() and ((g < -132) & (np.abs(want) > 1e-37)).any()
+    # g and u take one factor y = 1 / sqrt(1 + w^2), w = exp(-g / 2), each. The argument of
+    # w = 2^a, a = -g log2(e) / 2 - 63 (w is held 2^63 smaller), is rounded, 2^-24 of up to
+    # 0.72 |g| + 63, and so is the constant: (|g| + 44) 2^-24 of w, twice that of the result;
+    # exponential and root a unit (2^-23) each and twice, 1 + w^2, and three products half a unit:
+    # 50 units in all. y is no longer a normal number below g = -174, and 0 below -176, where
+    # |g / (1 + exp(-g))| < 177 exp(-176) < 2^-246. Then the output's rounding, to a
+    # multiple of 2^-133 at least.
+    e = np.abs(want) * (np.abs(g) + 50) * 2.0 ** -23 + 2.0 ** -246 * np.abs(u) + 2.0 ** -149
+    e = e + 2.0 ** -8 * (np.abs(want) + e) + 2.0 ** -134
+    assert close(run_gemm(x, w, xfmt, M, K, N, 1, BF16), want, e).all()
+
+
 @pytest.mark.parametrize("rows,experts,top,M", [(3, 4, 2, 130), (200, 8, 2, 700), (500, 4, 1, 1500)])
 @pytest.mark.parametrize("xfmt", [E2M1, E4M3])
 def test_silu_float32_of_experts(rows, experts, top, M, xfmt):
@@ -97,5 +118,6 @@ def test_silu_of_infinite_and_nan_sums():
             w = [np.zeros((2 * M, K // 2), np.uint8), np.full((2 * M, ref.pitch(K)), 127, np.uint8)]
             w[0][:M, 0], w[1][:M, 0] = np.where(np.arange(M) % 2, 7, 15), 200
             w[0][M:, 0], w[1][M:, 0] = 2, 60
-            got = run_gemm(x, w, xfmt, M, K, N, 1, F32)
-            assert (got[:, 1::2] == np.inf).all() and np.isnan(got[:, 0::2]).all()
+            for dtype in (F32, BF16):
+                got = run_gemm(x, w, xfmt, M, K, N, 1, dtype)
+                assert (got[:, 1::2] == np.inf).all() and np.isnan(got[:, 0::2]).all()
