@@ -558,10 +558,11 @@ int qmx_dequant(int fmt, const void *codes, const void *scales, int64_t rows, in
  * M..2M-1, both float32 sums,  y = g / (1 + exp(-g)) * u  (of these sums within
  * 8 roundings to float32 for QG_F32; for QG_BF16 within 2^-15 |y| + 2^-246 |u|
  * and the rounding to it; NaN where g is -infinity).
- * Products of elements and scales are exact; sums are float32, where an
- * instruction adds the products of 64 or 128 inputs at once and keeps 24
- * bits below the largest of them and the sum: every output is within
- * (K / 32 + 4) * 2^-23 * sum_k |x w| of the exact sum before the activation
+ * Products of elements and scales are exact; sums are float32, to which blocks of
+ * 32 inputs are added one by one (of e4m3 rows twice): a product that is 2^-27 of
+ * the sum so far or less may be dropped, and each such addition rounds. Every
+ * output is within (K / 8 + 4) * 2^-23 * sum_k |x w| + K * 2^-148 of the exact sum
+ * (where sum_k |x w| is out of float32's range, infinity or NaN) before the activation
  * and the rounding to `dtype`. A block with s = 255, or an e4m3 NaN, makes the
  * outputs of its row (of x) or column (of W) NaN. Results repeat from call
  * to call; the rounding of a row depends on how many rows there are.
