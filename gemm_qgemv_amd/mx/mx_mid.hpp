@@ -35,7 +35,9 @@ struct MxMidLds {
 };
 
 // A wave's memory operations since it asked for the x of the stage at place u of
-// four: a stage asks for x (FL loads) and MI weights, one in two for MI scales.
+// four: a stage asks for x (FL loads) and MI weights, one in two for MI scales. They
+// come in order, so that the wait holds only if a stage asks for x first, whatever
+// the compiler's scheduler does: mx_x_first stands behind it.
 template <int MI, int FL, int D>
 __host__ __device__ constexpr int mx_mid_since(int u)
 {
@@ -43,6 +45,8 @@ __host__ __device__ constexpr int mx_mid_since(int u)
     for (int s = u + 8 - D + 1; s < u + 8; ++s) n += MI + (s % 2 == 0 ? MI : 0) + (s > u + 8 - D + 1 ? FL : 0);
     return n;
 }
+
+__device__ __forceinline__ void mx_x_first() { __builtin_amdgcn_sched_barrier(0); }
 
 template <int XF, typename T, bool SILU, bool GROUPED, int MI, int NJ>
 __global__ __launch_bounds__(kMidThreads, 2) void mx_mid_kernel(MxGemmParams p)
@@ -174,6 +178,7 @@ __global__ __launch_bounds__(kMidThreads, 2) void mx_mid_kernel(MxGemmParams p)
     Weights R[2];
     Scales S[2];
     for (int t = 0; t < D - 1; ++t) fill(t);
+    mx_x_first();
     load(R[0], 0);
     load_scales(S[0], 0);
     mx_meet<(D - 2) * FL + MI * 2>();
@@ -181,6 +186,7 @@ __global__ __launch_bounds__(kMidThreads, 2) void mx_mid_kernel(MxGemmParams p)
         constexpr int u = decltype(place)::value;    // t % 4
         mx_meet<mx_mid_since<MI, FL, D>(u)>();
         fill(t + D - 1);
+        mx_x_first();
         load(R[u % 2 ^ 1], t + 1);
         if constexpr (u % 2 == 0) load_scales(S[u / 2 ^ 1], t / 2 + 1);
         __builtin_amdgcn_sched_barrier(0);
