@@ -15,7 +15,7 @@ struct CombineParams {
     const int32_t *slots;
     const float *weights;
     void *out;
-    int64_t rows, M, pairs;
+    int64_t M, pairs;
     int32_t top;
     uint32_t pieces;         // (token, run of 8 outputs) pairs of this launch
     FastDiv per_row;         // runs of a token

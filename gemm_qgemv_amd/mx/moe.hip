@@ -175,7 +175,6 @@ int qmoe_combine(int dtype, const void *y, const int32_t *slots, const float *we
         p.slots = slots + first * top;
         p.weights = weights + first * top;
         p.out = static_cast<char *>(out) + first * M * osize;
-        p.rows = n;
         p.M = M;
         p.pairs = pairs;
         p.top = top;
