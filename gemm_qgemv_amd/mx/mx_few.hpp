@@ -7,11 +7,17 @@
 // waves so takes 16 MI * 4 / KS outputs. A weight row's 64 bytes of a step are read
 // by its four lanes, its scales of a run by one load of 16 bytes (asked for step by
 // step, 4 bytes of each row, they cost a third of the time: 151936 x 2048, one row
-// 49 us, 33 without any scales; now 30, 5.4 TB/s). The loop has no branches, so that
-// the compiler knows how many loads are under way. Bound by HBM where the weights
-// are many: 17408 x 5120 13.2 us for one row and 17.5 for 16 (3.5 and 2.7 TB/s), 64 x 8
-// rows of 128 experts, 1024 -> 2048, 30 us (4.7 TB/s); 6144 x 2048, one row, 5.8 us
-// a call among others is the launch.
+// 49 us, 33 without any scales; now 30). The loop has no branches, so that
+// the compiler knows how many loads are under way.
+//
+// Measured a call among others, e4m3 rows, on weights that come from memory (copies of them
+// in turn) and in brackets on the same ones again, which the last cache holds in part.
+// Bound by HBM where the weights are many: 151936 x 2048, one row, 33 us [30], 5.0 TB/s; 64
+// x 8 rows of 128 experts, 1024 -> 2048, 30 us [27], 4.8 TB/s. 17408 x 5120 are 47 MB, 9 us
+// of HBM: one row 17 us [12], 16 rows 23 [17]; there a launch, a wave's first loads and
+// the sum of the waves are a large part, and with 16 rows as many bytes of rows as of
+// weights, loaded and split for every 32 outputs anew. 6144 x 2048, one row, 6.5 us is the
+// launch.
 #pragma once
 
 #include "mx_gemm.hpp"

@@ -20,6 +20,8 @@ int64_t usual_rows(const Call &c) { return c.grouped ? ceil_div(c.N, c.experts) 
 //  few against mid     2048 x 8192 x 24: 10 against 19 us [7.6, 17]; 6144 x 2048 x 60:
 //                      12, 11 [9, 8]; 17408 x 5120 x 24: 32, 21 [22, 18]
 //  few against tiles   1024 x 2048 x 256: 9, 17.5 [7.5, 12]; 2048 x 8192 x 200: 45, 51 [33, 29]
+//                      (6.5 pieces a compute unit: tiles of both, though e4m3 rows still
+//                      do better in pieces there; the limit is one for both)
 //  few of one block of outputs a wave against two   2048 x 8192 x 16: 9.3, 11.4 [7.4, 9.6];
 //                      17408 x 5120 x 16: 21, 18 [15, 15]; 151936 x 2048 x 1: 33, 30 [28, 26];
 //                      2048 x 8192 x 77: 21, 19 [16, 16]

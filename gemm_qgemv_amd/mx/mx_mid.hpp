@@ -10,10 +10,13 @@
 // are of the gate and of the up matrix in turn. The parts' sums are added through
 // LDS in a fixed order.
 //
-// Two parts of two waves, so that a compute unit holds two workgroups of most sizes,
-// whose loads and products overlap (77 x 2 x 17408 x 5120, e4m3: 58 us, with four parts
-// 72). Bound by the loads' latency and the vector instructions that split e4m3 rows in
-// turn: 17408 x 5120 x 90 rows e2m1 24 us (1.9 TB/s of weights), x 77 e4m3 37 us.
+// Two parts of two waves, so that a compute unit has room for two workgroups of most
+// sizes, whose loads and products overlap where there are as many (77 x 2 x 17408 x 5120,
+// e4m3, has 272 workgroups, so that most units hold one: 58 us, with four parts 72).
+// Bound by the loads' latency: weights are asked for one stage ahead, 16 KiB of them
+// a compute unit and workgroup, and a stage takes as long as they do (matrix and vector
+// instructions issue a fifth of the time each). 17408 x 5120 x 90 rows e2m1 22 us, 28
+// with weights that come from memory (1.7 TB/s of them), x 60 e4m3 32 and 34.
 #pragma once
 
 #include <type_traits>

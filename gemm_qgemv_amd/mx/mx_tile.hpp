@@ -19,11 +19,13 @@
 // in turn, so that a lane holds both numbers of an output.
 //
 // Measured: 10240 x 17408 x 5120 e2m1 480 us (3.8 PFLOP/s; the instruction alone reaches
-// 6.7), with SILU twice as many outputs 906; e4m3, two products each, 1265 (1.44, so
+// 6.7), with SILU twice as many outputs 923; e4m3, two products each, 1265 (1.44, so
 // 2.9 of 4.1). Of the 480 us the loads alone take 320, the products and LDS reads alone 370
-// and the stores, which nothing overlaps, 60. Experts, 4099 x 8 rows of 64, 2048 -> 2 x
-// 1024: 92 us evenly shared, 122 where a third of the experts' last tiles are nearly
-// empty. Each stage is one block of instructions: with a branch in it the
+// and the stores 60, which nothing overlaps: they leave the registers as they are
+// issued, but the wait in the next tile's first stage is one for all memory
+// operations. Experts of e2m1 rows, 64, 8 each, 2048 -> 2 x 1024: 96 us where 4096
+// rows fill every tile, 107 where 4099 leave a nearly empty one each, 123 unevenly liked; e4m3
+// 212, 229 and 243. Each stage is one block of instructions: with a branch in it the
 // compiler moves the products of all four steps behind it, and the matrix cores wait
 // while addresses are made (512 us). 256 x 128 tiles in three slots: 1024 x 2048 x 32768
 // with SILU 91 us instead of 79; 128 x 128, two workgroups a compute unit, 94.

@@ -4,8 +4,9 @@
 // 16 lanes take a row (one DPP row: maxima over it need no LDS), a lane every
 // 16th logit as an order-preserving integer, 0 for what cannot be chosen. Each
 // of the `top` rounds takes the largest number by four DPP maxima, then the
-// lowest index that has it by four minima. Bound by these instructions, not by
-// memory: 16411 x 256 bf16, 6 each, 13.6 us for 9 MB. (Lanes that sort their logits in a
+// lowest index that has it by four minima. Bound by these rounds, not by memory: 8
+// steps that wait for one another behind two passes over a lane's logits (vector
+// instructions issue 43% of the time); 16411 x 256 bf16, 6 each, 13.6 us for 9 MB. (Lanes that sort their logits in a
 // network first took three times as long: the conditions held for 16 numbers
 // at once do not fit in the scalar registers.)
 #pragma once
