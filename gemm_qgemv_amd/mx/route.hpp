@@ -114,6 +114,8 @@ __device__ __forceinline__ void route_row(const RouteParams &p, int64_t row)
 #pragma unroll
     for (int h = 0; h < H; ++h) w[h] = id[h] >= 0 ? expf(from_order_bits(got[h]) - m) : 0.0f;
     if (p.renorm) z = row16_sum(w[0] + w[1]);
+    // (one quotient a row: a weight has a rounding more than by a quotient of its own, beside
+    // those of its exponential and of the sum)
     const float inv = 1.0f / (z > 0.0f ? z : 1.0f);
 #pragma unroll
     for (int h = 0; h < H; ++h) {
